@@ -49,7 +49,7 @@ PAGE_H100_FUSED_US = 8.1
 # the files each kernel is built from; the hash also covers their compile flags
 KERNEL_SOURCES = {
     "decode_kernel": ["common.h", "kernels.h", "lds_dma.h", "exchange.h", "decode.hip"],
-    "gemm_bf16_kernel": ["common.h", "kernels.h", "lds_dma.h", "gemm.hip", "moe.hip"],
+    "gemm_bf16_kernel": ["common.h", "kernels.h", "lds_dma.h", "gemm_train.h", "gemm_kernel.h", "gemm.hip", "moe.hip"],
     "small_mlp2_kernel": ["common.h", "kernels.h", "small_mlp.hip"],
     "moe_router_mfma_kernel": ["common.h", "kernels.h", "lds_dma.h", "moe.hip"],
     "decode_w8_kernel": ["common.h", "kernels.h", "lds_dma.h", "exchange.h", "decode_w8.h", "decode_w8.hip"],

@@ -25,6 +25,13 @@ raises.
     fmlp_linear_bwd(x, W, b, act, dy)               -> (dx, dW, db): gradients of fmlp_linear
     fmlp_glu_bwd(x, Wg, Wu, Wd, gate_act, dy)       -> (dx, dWg, dWu, dWd): gradients of fmlp_glu
 
+    fmlp_glu_ckpt(x, Wg, Wu, Wd, gate_act)          -> (y, codes, scales): fmlp_glu that keeps g and u in 8 bits
+    fmlp_glu_ckpt_bwd(x, codes, scales, Wg, Wu, Wd, gate_act, dy)
+                                                    -> (dx, dWg, dWu, dWd) from that checkpoint
+    fmlp_grouped_linear(x, group_off, W, b, act)    y[r] = act(x[r] W[e]^T + b[e]), rows [off[e], off[e+1]) of group e
+    fmlp_grouped_linear_bwd(x, group_off, W, b, act, dy)
+                                                    -> (dx, dW, db): its gradients
+
 Activations: "none", "gelu_erf", "gelu_tanh", "relu", "silu".
 """
 from __future__ import annotations
@@ -48,6 +55,14 @@ __all__ = [
     "fmlp_glu_noalloc",
     "fmlp_linear_bwd",
     "fmlp_glu_bwd",
+    "fmlp_glu_ckpt",
+    "fmlp_glu_ckpt_bwd",
+    "fmlp_grouped_linear",
+    "fmlp_grouped_linear_bwd",
+    "bind_glu_ckpt",
+    "bind_glu_ckpt_bwd",
+    "bind_grouped_linear",
+    "bind_grouped_linear_bwd",
     "bind_linear_bwd",
     "bind_glu_bwd",
     "fmlp_moe_geglu",
@@ -138,6 +153,20 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = _sz
         for f in ("fmlp_linear", "fmlp_mlp2", "fmlp_geglu", "fmlp_glu", "fmlp_moe_geglu", "fmlp_moe_glu",
                   "fmlp_moe_route", "fmlp_set_path", "fmlp_set_cooperative_decode"):
+            getattr(L, f).restype = ctypes.c_int
+        L.fmlp_glu_ckpt.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]
+        L.fmlp_glu_ckpt_bwd.argtypes = [_p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p,
+                                        _sz, _p]
+        L.fmlp_grouped_linear.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _p, _p, _sz, _p]
+        L.fmlp_grouped_linear_bwd.argtypes = [_p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, ctypes.c_int32, _p, _p,
+                                              _p, _p, _sz, _p]
+        for f, a in (("fmlp_glu_ckpt_workspace_size", [_i64] * 3), ("fmlp_glu_ckpt_bwd_workspace_size", [_i64] * 3),
+                     ("fmlp_glu_ckpt_codes_size", [_i64] * 2), ("fmlp_glu_ckpt_scales_size", [_i64] * 2),
+                     ("fmlp_grouped_linear_workspace_size", [ctypes.c_int32]),
+                     ("fmlp_grouped_linear_bwd_workspace_size", [_i64] * 3 + [ctypes.c_int32, ctypes.c_int])):
+            getattr(L, f).argtypes = a
+            getattr(L, f).restype = _sz
+        for f in ("fmlp_glu_ckpt", "fmlp_glu_ckpt_bwd", "fmlp_grouped_linear", "fmlp_grouped_linear_bwd"):
             getattr(L, f).restype = ctypes.c_int
         L.fmlp_linear_w8.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p]
         L.fmlp_mlp2_w8.argtypes = [_p, _p, _p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _i64, _p, _p,
@@ -466,6 +495,180 @@ def fmlp_glu_bwd(x, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None):
 def bind_glu_bwd(x, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None) -> BoundCall:
     with torch.cuda.device(x.device):
         return _glu_bwd_call(x, Wg, Wu, Wd, gate_act, dy, out, workspace)
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert; the gated block with an 8-bit checkpoint
+# ---------------------------------------------------------------------------
+def _scratch(like: torch.Tensor, workspace, nbytes: int) -> torch.Tensor:
+    """The caller's workspace, or fresh memory of the current stream's pool: these calls need no initialised
+    header, and memory of a call's own is safe for captured graphs that replay on different streams."""
+    if workspace is not None:
+        if workspace.dtype != torch.uint8:
+            raise TypeError(f"workspace must be torch.uint8 (got {workspace.dtype})")
+        _same_device(like, workspace=workspace)
+        return _dev_tensor("workspace", workspace, torch.uint8)
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _same_device(like: torch.Tensor, **tensors) -> None:
+    for n, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{n} is on {t.device}, x on {like.device}")
+
+
+def _out(name, t, shape, like, dtype=torch.bfloat16) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dev_tensor(name, t, dtype)
+    _same_device(like, **{name: t})
+    if t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _grouped_args(x, group_off, W, b):
+    _dev_tensor("x", x)
+    _dev_tensor("W", W)
+    _dev_tensor("group_off", group_off, torch.int32)
+    _same_device(x, W=W, group_off=group_off, b=b)
+    if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
+        raise ValueError(f"x must be [R, K] and W [E, N, K], got {tuple(x.shape)} and {tuple(W.shape)}")
+    R, K = x.shape
+    E, N = W.shape[0], W.shape[1]
+    if group_off.shape != (E + 1,):
+        raise ValueError(f"group_off must be [{E + 1}] int32, got {tuple(group_off.shape)}")
+    if b is not None:
+        _dev_tensor("b", b)
+        if b.shape != (E, N):
+            raise ValueError(f"b must be [{E}, {N}], got {tuple(b.shape)}")
+    return R, K, N, E
+
+
+def _grouped_linear_call(x, group_off, W, b, act, out, workspace):
+    R, K, N, E = _grouped_args(x, group_off, W, b)
+    y = _out("out", out, (R, N), x)
+    L = lib()
+    ws = _scratch(x, workspace, L.fmlp_grouped_linear_workspace_size(E))
+    return BoundCall(L.fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K,
+                                             N, E, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device)),
+                     y, (x, group_off, W, b, ws))
+
+
+def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None):
+    """y[r] = act(x[r] W[e]^T + b[e]) for the rows [group_off[e], group_off[e+1]) of every group e.
+
+    x [R, K]; group_off int32 [E + 1] on the device; W [E, N, K]; b [E, N] or None -> y [R, N].  Rows outside every
+    group are not written: with out=None they hold whatever the new tensor held."""
+    with torch.cuda.device(x.device):
+        return _grouped_linear_call(x, group_off, W, b, act, out, workspace)()
+
+
+def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _grouped_linear_call(x, group_off, W, b, act, out, workspace)
+
+
+def _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace):
+    R, K, N, E = _grouped_args(x, group_off, W, b)
+    _dev_tensor("dy", dy)
+    _same_device(x, dy=dy)
+    if dy.shape != (R, N):
+        raise ValueError(f"dy must be [{R}, {N}], got {tuple(dy.shape)}")
+    dx, dW, db = out if out is not None else (None, None, None)
+    dx = _out("dx", dx, (R, K), x)
+    dW = _out("dW", dW, (E, N, K), x)
+    if b is not None or db is not None:
+        db = _out("db", db, (E, N), x)
+    L = lib()
+    ws = _scratch(x, workspace, L.fmlp_grouped_linear_bwd_workspace_size(R, K, N, E, ACT[act]))
+    return BoundCall(L.fmlp_grouped_linear_bwd, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act],
+                                                 dy.data_ptr(), R, K, N, E, dx.data_ptr(), dW.data_ptr(), _ptr(db),
+                                                 ws.data_ptr(), ws.numel(), _stream(x.device)),
+                     (dx, dW, db), (x, group_off, W, b, dy, ws))
+
+
+def fmlp_grouped_linear_bwd(x, group_off, W, b, act: str, dy, out=None, workspace=None):
+    """Gradients of fmlp_grouped_linear: returns (dx [R, K], dW [E, N, K], db [E, N], or None without b).  Rows of dx
+    outside every group are not written."""
+    with torch.cuda.device(x.device):
+        return _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace)()
+
+
+def bind_grouped_linear_bwd(x, group_off, W, b, act: str, dy, out=None, workspace=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace)
+
+
+def _ckpt_args(x, Wg, Wu, Wd):
+    for n, t in (("x", x), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd)):
+        _dev_tensor(n, t)
+    _same_device(x, Wg=Wg, Wu=Wu, Wd=Wd)
+    D, H = x.shape[-1], Wg.shape[0]
+    if Wg.shape != (H, D) or Wu.shape != (H, D) or Wd.shape != (D, H):
+        raise ValueError(f"shape mismatch: x[...,{D}] Wg{tuple(Wg.shape)} Wu{tuple(Wu.shape)} Wd{tuple(Wd.shape)}")
+    return x.numel() // D, D, H
+
+
+def _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace):
+    M, D, H = _ckpt_args(x, Wg, Wu, Wd)
+    y, codes, scales = out if out is not None else (None, None, None)
+    y = _out("y", y, x.shape, x)
+    codes = _out("codes", codes, (M, 2 * H), x, torch.uint8)
+    scales = _out("scales", scales, (M, 2 * ((H + 31) // 32)), x, torch.uint8)
+    L = lib()
+    ws = _scratch(x, workspace, L.fmlp_glu_ckpt_workspace_size(M, D, H))
+    return BoundCall(L.fmlp_glu_ckpt, (x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), ACT[gate_act], M, D, H,
+                                       y.data_ptr(), codes.data_ptr(), scales.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _stream(x.device)), (y, codes, scales), (x, Wg, Wu, Wd, ws))
+
+
+def fmlp_glu_ckpt(x, Wg, Wu, Wd, gate_act: str = "silu", out=None, workspace=None):
+    """fmlp_glu that keeps g = x Wg^T and u = x Wu^T in 8 bits for fmlp_glu_ckpt_bwd: returns (y, codes, scales).
+
+    codes uint8 [M, 2H] (E4M3, g then u), scales uint8 [M, 2 ceil(H / 32)]: value = e4m3(code) * 2**(scale - 127)
+    for the scale of its row and block of 32 hidden units."""
+    with torch.cuda.device(x.device):
+        return _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace)()
+
+
+def bind_glu_ckpt(x, Wg, Wu, Wd, gate_act: str = "silu", out=None, workspace=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace)
+
+
+def _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace):
+    M, D, H = _ckpt_args(x, Wg, Wu, Wd)
+    _dev_tensor("dy", dy)
+    codes = _w8_codes("codes", codes)
+    _dev_tensor("scales", scales, torch.uint8)
+    _same_device(x, dy=dy, codes=codes, scales=scales)
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must be {tuple(x.shape)}, got {tuple(dy.shape)}")
+    if codes.shape != (M, 2 * H) or scales.shape != (M, 2 * ((H + 31) // 32)):
+        raise ValueError(f"codes must be [{M}, {2 * H}] and scales [{M}, {2 * ((H + 31) // 32)}], got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    dx, dWg, dWu, dWd = out if out is not None else (None, None, None, None)
+    dx, dWg, dWu, dWd = (_out(n, t, s, x) for n, t, s in (("dx", dx, x.shape), ("dWg", dWg, (H, D)),
+                                                          ("dWu", dWu, (H, D)), ("dWd", dWd, (D, H))))
+    L = lib()
+    ws = _scratch(x, workspace, L.fmlp_glu_ckpt_bwd_workspace_size(M, D, H))
+    return BoundCall(L.fmlp_glu_ckpt_bwd, (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), Wg.data_ptr(),
+                                           Wu.data_ptr(), Wd.data_ptr(), ACT[gate_act], dy.data_ptr(), M, D, H,
+                                           dx.data_ptr(), dWg.data_ptr(), dWu.data_ptr(), dWd.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), _stream(x.device)),
+                     (dx, dWg, dWu, dWd), (x, codes, scales, Wg, Wu, Wd, dy, ws))
+
+
+def fmlp_glu_ckpt_bwd(x, codes, scales, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None):
+    """Gradients of the gated block at the g and u that fmlp_glu_ckpt kept: returns (dx, dWg, dWu, dWd)."""
+    with torch.cuda.device(x.device):
+        return _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)()
+
+
+def bind_glu_ckpt_bwd(x, codes, scales, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)
 
 
 def fmlp_moe_workspace_size(T, D, H, E, top_k) -> int:

@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfmlp.so")
-SOURCES = ["abi.cpp", "gemm.hip", "decode.hip", "decode_w8.hip", "small_mlp.hip", "moe.hip", "transpose.hip", "noalloc.hip",
+SOURCES = ["abi.cpp", "train.cpp", "gemm.hip", "gemm_train.hip", "grouped.hip", "decode.hip", "decode_w8.hip", "small_mlp.hip", "moe.hip", "transpose.hip", "noalloc.hip",
            "glu_fused.hip"]
 ARCH = "gfx950"
 # Per-source flags.  The GEMM main loop is written in issue order (fragment
@@ -29,6 +29,7 @@ ARCH = "gfx950"
 # order keeps them in place.  The FP8 decode loop is written the same way (one
 # register batch's loads issued before the previous batch is converted).
 EXTRA_FLAGS = {"gemm.hip": ["-mllvm", "-enable-misched=0"],
+               "gemm_train.hip": ["-mllvm", "-enable-misched=0"],
                "decode_w8.hip": ["-mllvm", "-enable-misched=0"]}
 
 

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <string>
 
+#include "abi_calls.h"
 #include "decode_w8.h"
 #include "kernels.h"
 
@@ -23,13 +24,18 @@ thread_local std::string g_last_error;
 thread_local int g_path = 0;   // 0 auto, 1 decode, 2 two-GEMM, 3 small fused, 4 fused gated block
 thread_local bool g_coop = false;   // cooperative launch of the one-launch decode forms
 
-constexpr int kPathAuto = 0, kPathDecode = 1, kPathGemm = 2, kPathSmall = 3, kPathFused = 4;
-constexpr int64_t kDecodeMaxM = 16;
-constexpr int64_t kSmallMaxDim = 128;
-constexpr int64_t kMaxDim = int64_t(1) << 31;   // bound on a token count
-constexpr int64_t kMaxInner = int64_t(1) << 22; // bound on an inner dimension: a 256-row
-                                                // operand tile spans < 2^31 bytes
-constexpr size_t kHeader = kWorkspaceHeaderBytes;  // barrier / error words
+// ---- device check (cached per device) ---------------------------------------
+struct DevInfo {
+  bool probed = false;
+  bool gfx950 = false;
+  int cus = 0;
+};
+std::mutex g_dev_mu;
+DevInfo g_dev[64];
+
+}  // namespace
+
+namespace fmlp {
 
 fmlp_status fail(fmlp_status s, const char* fmt, ...) {
   char buf[512];
@@ -46,66 +52,7 @@ fmlp_status ok() {
   return FMLP_OK;
 }
 
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define REQUIRE_PTR(p)                                                      \
-  do {                                                                      \
-    if ((p) == nullptr) return fail(FMLP_E_NULL, "%s is NULL", #p);         \
-    if (!aligned16(p)) return fail(FMLP_E_ALIGN, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
-// Token-sized buffers (activations, outputs, routes) hold nothing when there
-// are no tokens: NULL is then accepted, a misaligned pointer is still not.
-#define TOKEN_PTR(p, rows)                                                  \
-  do {                                                                      \
-    if ((rows) > 0) REQUIRE_PTR(p);                                         \
-    else if ((p) != nullptr && !aligned16(p))                               \
-      return fail(FMLP_E_ALIGN, "%s is not 16-byte aligned", #p);           \
-  } while (0)
-
-#define OPTIONAL_PTR(p)                                                     \
-  do {                                                                      \
-    if ((p) != nullptr && !aligned16(p))                                    \
-      return fail(FMLP_E_ALIGN, "%s is not 16-byte aligned", #p);           \
-  } while (0)
-
-fmlp_status check_rows(const char* name, int64_t v) {
-  if (v < 0 || v >= kMaxDim) return fail(FMLP_E_SHAPE, "%s=%lld is out of range", name, (long long)v);
-  return FMLP_OK;
-}
-
-fmlp_status check_inner(const char* name, int64_t v) {
-  if (v <= 0 || v >= kMaxInner)
-    return fail(FMLP_E_SHAPE, "%s=%lld must be in [8, 2^22)", name, (long long)v);
-  if (v % 8 != 0) return fail(FMLP_E_ALIGN, "%s=%lld is not a multiple of 8", name, (long long)v);
-  return FMLP_OK;
-}
-
-fmlp_status check_act(int act, const char* name = "act") {
-  if (act != FMLP_ACT_NONE && act != FMLP_ACT_GELU_ERF && act != FMLP_ACT_GELU_TANH &&
-      act != FMLP_ACT_RELU && act != FMLP_ACT_SILU)
-    return fail(FMLP_E_ARG, "%s=%d is not an fmlp_act", name, act);
-  return FMLP_OK;
-}
-
-#define TRY(expr)                              \
-  do {                                         \
-    fmlp_status s_ = (expr);                   \
-    if (s_ != FMLP_OK) return s_;              \
-  } while (0)
-
-// ---- device check (cached per device) ---------------------------------------
-struct DevInfo {
-  bool probed = false;
-  bool gfx950 = false;
-  int cus = 0;
-};
-std::mutex g_dev_mu;
-DevInfo g_dev[64];
-
-fmlp_status check_device(int* cus_out = nullptr) {
+fmlp_status check_device(int* cus_out) {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess || dev < 0) return fail(FMLP_E_DEVICE, "no current HIP device (%s)", hipGetErrorString(e));
@@ -187,9 +134,6 @@ hipError_t gemm_glu_gateup(const uint16_t* x, const uint16_t* Wg, const uint16_t
                      dense_params(x, D, Wg, Wu, nullptr, m, H, M, H, D, gate_act, cus), s);
 }
 
-}  // namespace
-
-namespace fmlp {
 // The status and detail text of a failure found outside this file (the
 // no-allocation entry point), for fmlp_last_error().
 fmlp_status record_error(fmlp_status s, const char* msg) { return fail(s, "%s", msg); }
@@ -526,14 +470,7 @@ fmlp_status fmlp_moe_route(const fmlp_bf16* x, const fmlp_bf16* Wr, int64_t T, i
 // ---------------------------------------------------------------------------
 // Backward pass
 // ---------------------------------------------------------------------------
-namespace {
-// Token counts of a backward call bound the contraction over tokens, which the
-// GEMM reads with 32-bit offsets like any inner dimension.
-constexpr int64_t kBwdMaxTokens = kMaxInner;
-
-size_t ws_bf16(int64_t rows, int64_t cols) { return round_up((size_t)rows * (size_t)cols * 2, 256); }
-int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
-
+namespace fmlp {
 // Weight gradients contract over the tokens: C[R, Cc] = A[R, T] . B[Cc, T]^T
 // with both operands transposed to token-contiguous rows (T = tokens padded
 // to 8).  Few output tiles over a long token range leave most CUs idle (the
@@ -606,6 +543,69 @@ hipError_t gemm_wgrad_kmajor(const uint16_t* A, int64_t lda, const uint16_t* B, 
   return launch_sum_parts(parts, P, R * Cc, R * Cc, C, s);
 }
 
+// The last steps of both gated backward passes, from m [M, H] and dg | du
+// [M, 2H]: dx and the three weight gradients.  scratch: glu_products_scratch
+// bytes, the transposed operands of shapes off the 256x256 tiles and the parts
+// of split weight gradients.
+struct ProductsLayout {
+  size_t wgut, dyt, mt, dgdut, xt, parts, total;
+};
+ProductsLayout products_layout(int64_t M, int64_t D, int64_t H) {
+  const int64_t Mp = pad8(M);
+  ProductsLayout L;
+  size_t o = 0;
+  L.wgut = o;  o += ws_bf16(D, 2 * H);
+  L.dyt = o;   o += ws_bf16(D, Mp);
+  L.mt = o;    o += ws_bf16(H, Mp);
+  L.dgdut = o; o += ws_bf16(2 * H, Mp);
+  L.xt = o;    o += ws_bf16(D, Mp);
+  L.parts = o; o += std::max(wgrad_parts_bytes(D, Mp, H), wgrad_parts_bytes(H, Mp, D));
+  L.total = o;
+  return L;
+}
+size_t glu_products_scratch(int64_t M, int64_t D, int64_t H) { return products_layout(M, D, H).total; }
+
+fmlp_status glu_bwd_products(const uint16_t* x, const uint16_t* dy, const uint16_t* Wg, const uint16_t* Wu,
+                             const uint16_t* m, const uint16_t* dgdu, int64_t M, int64_t D, int64_t H, uint16_t* dx,
+                             uint16_t* dWg, uint16_t* dWu, uint16_t* dWd, void* scratch, int cus, hipStream_t s) {
+  const int64_t Mp = pad8(M);
+  const ProductsLayout L = products_layout(M, D, H);
+  auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(static_cast<char*>(scratch) + off); };
+  uint16_t *wgut = at(L.wgut), *dyt = at(L.dyt), *mt = at(L.mt), *dgdut = at(L.dgdut), *xt = at(L.xt);
+  float* parts = reinterpret_cast<float*>(at(L.parts));
+  // dx = dg Wg + du Wu = [dg | du] [Wg ; Wu]: one GEMM over 2H (the weights
+  // read k-major, B switching from Wg to Wu at row H, or transposed first)
+  if (H % 64 == 0 && gemm_bkmajor_ok(M, D, 2 * H, H, cus)) {
+    HIP_TRY(gemm_bkmajor(dgdu, Wg, Wu, H, M, D, 2 * H, dx, cus, s), "glu_bwd dx launch");
+  } else {
+    HIP_TRY(launch_transpose(Wg, H, D, D, wgut, 2 * H, H, s), "glu_bwd transpose Wg");
+    HIP_TRY(launch_transpose(Wu, H, D, D, wgut + H, 2 * H, H, s), "glu_bwd transpose Wu");
+    HIP_TRY(gemm_linear(dgdu, wgut, nullptr, FMLP_ACT_NONE, M, 2 * H, D, dx, cus, s),
+            "glu_bwd dx launch");
+  }
+  // weight gradients: contractions over the token rows (both operands read
+  // k-major, or transposed first)
+  if (wgrad_kmajor_ok(D, M, H, D, H, cus)) {
+    HIP_TRY(gemm_wgrad_kmajor(dy, D, m, H, D, M, H, dWd, parts, cus, s), "glu_bwd dWd launch");
+  } else {
+    HIP_TRY(launch_transpose(dy, M, D, D, dyt, Mp, Mp, s), "glu_bwd transpose dy");
+    HIP_TRY(launch_transpose(m, M, H, H, mt, Mp, Mp, s), "glu_bwd transpose m");
+    HIP_TRY(gemm_wgrad(dyt, mt, D, Mp, H, dWd, parts, cus, s), "glu_bwd dWd launch");
+  }
+  if (wgrad_kmajor_ok(H, M, D, 2 * H, D, cus)) {
+    HIP_TRY(gemm_wgrad_kmajor(dgdu, 2 * H, x, D, H, M, D, dWg, parts, cus, s), "glu_bwd dWg launch");
+    HIP_TRY(gemm_wgrad_kmajor(dgdu + H, 2 * H, x, D, H, M, D, dWu, parts, cus, s), "glu_bwd dWu launch");
+  } else {
+    HIP_TRY(launch_transpose(dgdu, M, 2 * H, 2 * H, dgdut, Mp, Mp, s), "glu_bwd transpose dg|du");
+    HIP_TRY(launch_transpose(x, M, D, D, xt, Mp, Mp, s), "glu_bwd transpose x");
+    HIP_TRY(gemm_wgrad(dgdut, xt, H, Mp, D, dWg, parts, cus, s), "glu_bwd dWg launch");
+    HIP_TRY(gemm_wgrad(dgdut + H * Mp, xt, H, Mp, D, dWu, parts, cus, s), "glu_bwd dWu launch");
+  }
+  return ok();
+}
+}  // namespace fmlp
+
+namespace {
 struct LinearBwdLayout {
   size_t dz, wt, dzt, xt, parts, total;
 };
@@ -623,39 +623,19 @@ LinearBwdLayout linear_bwd_layout(int64_t M, int64_t K, int64_t N) {
 }
 
 struct GluBwdLayout {
-  size_t wdt, dm, m, dgdu, wgut, dyt, mt, dgdut, xt, parts, total;
+  size_t wdt, dm, m, dgdu, scratch, total;
 };
 GluBwdLayout glu_bwd_layout(int64_t M, int64_t D, int64_t H) {
-  const int64_t Mp = pad8(M);
   GluBwdLayout L;
   size_t o = kHeader;
-  L.wdt = o;   o += ws_bf16(H, D);
-  L.dm = o;    o += ws_bf16(M, H);
-  L.m = o;     o += ws_bf16(M, H);
-  L.dgdu = o;  o += ws_bf16(M, 2 * H);
-  L.wgut = o;  o += ws_bf16(D, 2 * H);
-  L.dyt = o;   o += ws_bf16(D, Mp);
-  L.mt = o;    o += ws_bf16(H, Mp);
-  L.dgdut = o; o += ws_bf16(2 * H, Mp);
-  L.xt = o;    o += ws_bf16(D, Mp);
-  L.parts = o; o += std::max(wgrad_parts_bytes(D, Mp, H), wgrad_parts_bytes(H, Mp, D));
+  L.wdt = o;     o += ws_bf16(H, D);
+  L.dm = o;      o += ws_bf16(M, H);
+  L.m = o;       o += ws_bf16(M, H);
+  L.dgdu = o;    o += ws_bf16(M, 2 * H);
+  L.scratch = o; o += glu_products_scratch(M, D, H);
   L.total = o;
   return L;
 }
-
-fmlp_status check_workspace(void* workspace, size_t workspace_bytes, size_t need) {
-  if (need == 0) return FMLP_OK;
-  if (workspace == nullptr) return fail(FMLP_E_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
-  if (!aligned16(workspace)) return fail(FMLP_E_ALIGN, "workspace is not 16-byte aligned");
-  if (workspace_bytes < need) return fail(FMLP_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-  return FMLP_OK;
-}
-
-#define HIP_TRY(expr, what)                               \
-  do {                                                    \
-    hipError_t e_ = (expr);                               \
-    if (e_ != hipSuccess) return launched(e_, what);      \
-  } while (0)
 }  // namespace
 
 extern "C" {
@@ -769,7 +749,6 @@ fmlp_status fmlp_glu_bwd(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf1
   }
   char* ws = static_cast<char*>(workspace);
   auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
-  const int64_t Mp = pad8(M);
   // dm = dy Wd: the contraction runs over Wd's rows (Wd read k-major, or
   // transposed first where the GEMM runs on smaller tiles)
   if (gemm_bkmajor_ok(M, H, D, 0, cus)) {
@@ -786,36 +765,7 @@ fmlp_status fmlp_glu_bwd(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf1
   p.ldc2 = 2 * H;
   HIP_TRY(launch_gemm(GEMM_OUT_DGLU, false, false, choose_tile(M, (H + 127) / 128, cus), p, s),
           "glu_bwd gate+up launch");
-  // dx = dg Wg + du Wu = [dg | du] [Wg ; Wu]: one GEMM over 2H (the weights
-  // read k-major, B switching from Wg to Wu at row H, or transposed first)
-  if (H % 64 == 0 && gemm_bkmajor_ok(M, D, 2 * H, H, cus)) {
-    HIP_TRY(gemm_bkmajor(at(L.dgdu), Wg, Wu, H, M, D, 2 * H, dx, cus, s), "glu_bwd dx launch");
-  } else {
-    HIP_TRY(launch_transpose(Wg, H, D, D, at(L.wgut), 2 * H, H, s), "glu_bwd transpose Wg");
-    HIP_TRY(launch_transpose(Wu, H, D, D, at(L.wgut) + H, 2 * H, H, s), "glu_bwd transpose Wu");
-    HIP_TRY(gemm_linear(at(L.dgdu), at(L.wgut), nullptr, FMLP_ACT_NONE, M, 2 * H, D, dx, cus, s),
-            "glu_bwd dx launch");
-  }
-  // weight gradients: contractions over the token rows (both operands read
-  // k-major, or transposed first)
-  float* parts = reinterpret_cast<float*>(ws + L.parts);
-  if (wgrad_kmajor_ok(D, M, H, D, H, cus)) {
-    HIP_TRY(gemm_wgrad_kmajor(dy, D, at(L.m), H, D, M, H, dWd, parts, cus, s), "glu_bwd dWd launch");
-  } else {
-    HIP_TRY(launch_transpose(dy, M, D, D, at(L.dyt), Mp, Mp, s), "glu_bwd transpose dy");
-    HIP_TRY(launch_transpose(at(L.m), M, H, H, at(L.mt), Mp, Mp, s), "glu_bwd transpose m");
-    HIP_TRY(gemm_wgrad(at(L.dyt), at(L.mt), D, Mp, H, dWd, parts, cus, s), "glu_bwd dWd launch");
-  }
-  if (wgrad_kmajor_ok(H, M, D, 2 * H, D, cus)) {
-    HIP_TRY(gemm_wgrad_kmajor(at(L.dgdu), 2 * H, x, D, H, M, D, dWg, parts, cus, s), "glu_bwd dWg launch");
-    HIP_TRY(gemm_wgrad_kmajor(at(L.dgdu) + H, 2 * H, x, D, H, M, D, dWu, parts, cus, s), "glu_bwd dWu launch");
-  } else {
-    HIP_TRY(launch_transpose(at(L.dgdu), M, 2 * H, 2 * H, at(L.dgdut), Mp, Mp, s), "glu_bwd transpose dg|du");
-    HIP_TRY(launch_transpose(x, M, D, D, at(L.xt), Mp, Mp, s), "glu_bwd transpose x");
-    HIP_TRY(gemm_wgrad(at(L.dgdut), at(L.xt), H, Mp, D, dWg, parts, cus, s), "glu_bwd dWg launch");
-    HIP_TRY(gemm_wgrad(at(L.dgdut) + H * Mp, at(L.xt), H, Mp, D, dWu, parts, cus, s), "glu_bwd dWu launch");
-  }
-  return ok();
+  return glu_bwd_products(x, dy, Wg, Wu, at(L.m), at(L.dgdu), M, D, H, dx, dWg, dWu, dWd, at(L.scratch), cus, s);
 }
 
 }  // extern "C"
@@ -832,13 +782,6 @@ extern "C" size_t fmlp_w8_workspace_size(int64_t M, int64_t H) {
 }
 
 namespace {
-
-#define SCALE_PTR(p)                                                        \
-  do {                                                                      \
-    if ((p) == nullptr) return fail(FMLP_E_NULL, "%s is NULL", #p);         \
-    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)                         \
-      return fail(FMLP_E_ALIGN, "%s is not 4-byte aligned", #p);            \
-  } while (0)
 
 fmlp_status check_w8_rows(int64_t M) {
   TRY(check_rows("M", M));

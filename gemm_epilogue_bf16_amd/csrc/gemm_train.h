@@ -1,0 +1,59 @@
+// Launch interface of the GEMM forms behind the grouped products and the gated
+// block with an 8-bit checkpoint (gemm_train.hip).  Internal to the library,
+// like kernels.h; not part of the public ABI.
+#pragma once
+
+#include "kernels.h"
+
+namespace fmlp {
+
+// Output kinds beyond GemmOut.
+constexpr int GEMM_OUT_GLU_SAVE = 5;     // GEMM_OUT_GEGLU that also writes g and u as E4M3 codes with block scales
+constexpr int GEMM_OUT_DGLU_SAVED = 6;   // acc = dm; g and u come from those codes: C = m = act(g) * u,
+                                         // C2 = [dm * u * act'(g) | dm * act(g)]
+
+// Hidden units of one row that share a checkpoint scale.
+constexpr int kCkptBlock = 32;
+
+// GemmParams::kmajor bit 2: ragged weight gradient.  Both operands are k-major
+// and every group has its own range of k rows, [group_off[g], group_off[g+1]):
+// C[g] [M, N] = A[rows of g]^T . B[rows of g], zeros for a group without rows.
+constexpr int kKmajorRagged = 4;
+
+struct GemmTrainParams : GemmParams {
+  uint8_t* codes;              // checkpoint: E4M3 codes [rows, 2N], g in columns [0, N), u in [N, 2N)
+  uint8_t* qscale;             // and scale exponents (+ 127) [rows, 2 ceil(N / kCkptBlock)]
+  int64_t stride_bias;         // grouped: elements between consecutive groups' biases
+  int64_t stride_c;            // ragged: elements between consecutive groups' outputs
+  const int64_t* work_off;     // ragged: [groups + 1] prefix of the stages of one tile of each group (see GroupPlan)
+};
+
+// y = act(x W[g]^T + b[g]) over each group's rows (GEMM_OUT_BF16), its dz
+// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2).  tile:
+// TILE_128x128 or TILE_256x256; with kmajor = 2 TILE_128x128 stands for a
+// 128 x 256 tile (the k-major operand's tile is 256 columns wide).
+hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
+// The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
+hipError_t launch_gemm_ragged(int out_kind, const GemmTrainParams& p, hipStream_t s);
+// GEMM_OUT_GLU_SAVE, and GEMM_OUT_DGLU_SAVED (kmajor 0 or 2).
+hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Helpers of the grouped products (grouped.hip).
+// ---------------------------------------------------------------------------
+// What the kernels of a call read about its groups, made on the device from the
+// caller's offsets: clamped into [0, R] and made nondecreasing (a bad table
+// gives wrong rows, never an access outside the buffers), the prefix of the
+// groups' bm-row tiles, and the prefix of max(stages, split) 64-row stages.
+struct GroupPlan {
+  int32_t* group_off;   // [E + 1]
+  int32_t* tile_off;    // [E + 1]
+  int64_t* work_off;    // [E + 1]
+};
+hipError_t launch_group_plan(const int32_t* off, int64_t R, int E, int bm, int split, const GroupPlan& plan,
+                             hipStream_t s);
+// db[e, n] = bf16(sum of dz[r, n] over group e's rows), fp32, a fixed order.
+hipError_t launch_group_colsum(const uint16_t* dz, const int32_t* group_off, int E, int64_t N, uint16_t* db,
+                               hipStream_t s);
+
+}  // namespace fmlp

@@ -1,0 +1,73 @@
+// The GEMM forms of the grouped products and of the gated block with an 8-bit
+// checkpoint: instantiations of gemm_kernel.h.
+#include "gemm_kernel.h"
+
+namespace fmlp {
+
+namespace {
+
+// one kernel per activation (see GACT in gemm_kernel.h)
+template <class F>
+hipError_t by_act(int act, F f) {
+  switch (act) {
+    case ACT_NONE: return f(std::integral_constant<int, ACT_NONE>{});
+    case ACT_GELU_ERF: return f(std::integral_constant<int, ACT_GELU_ERF>{});
+    case ACT_GELU_TANH: return f(std::integral_constant<int, ACT_GELU_TANH>{});
+    case ACT_RELU: return f(std::integral_constant<int, ACT_RELU>{});
+    case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s) {
+  const bool big = tile == TILE_256x256;
+  if (!big && tile != TILE_128x128) return hipErrorInvalidValue;
+  if (out_kind == GEMM_OUT_BF16 && p.kmajor == 2) {
+    if (p.bias != nullptr || p.act != ACT_NONE) return hipErrorInvalidValue;
+    return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s)
+               : launch_cfg<128, 256, 2, 4, 64, 3, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s);
+  }
+  if (p.kmajor != 0) return hipErrorInvalidValue;
+  if (out_kind == GEMM_OUT_BF16)
+    return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s)
+               : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s);
+  if (out_kind == GEMM_OUT_DACT)
+    return by_act(p.act, [&](auto a) {
+      return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s)
+                 : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_DACT, false, true, a.value>(p, s);
+    });
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemm_ragged(int out_kind, const GemmTrainParams& p, hipStream_t s) {
+  if (p.kmajor != (3 | kKmajorRagged) || p.groups < 1 || p.work_off == nullptr) return hipErrorInvalidValue;
+  if (out_kind == GEMM_OUT_BF16 && p.ksplit <= 1 && p.act == ACT_NONE && p.bias == nullptr)
+    return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, false, ACT_NONE, false, 3 | kKmajorRagged>(p, s);
+  if (out_kind == GEMM_OUT_F32_SCALED && p.row_scale == nullptr)
+    return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_F32_SCALED, false, false, ACT_NONE, false, 3 | kKmajorRagged>(p, s);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s) {
+  const bool big = tile == TILE_256x256;
+  if (!big && tile != TILE_128x128) return hipErrorInvalidValue;
+  if (p.codes == nullptr || p.qscale == nullptr) return hipErrorInvalidValue;
+  if (out_kind == GEMM_OUT_GLU_SAVE && p.kmajor == 0)
+    return by_act(p.act, [&](auto a) {
+      return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s)
+                 : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s);
+    });
+  if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 2 && big)
+    return by_act(p.act, [&](auto a) {
+      return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value, false, 2>(p, s);
+    });
+  if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 0 && !big)
+    return by_act(p.act, [&](auto a) {
+      return launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_DGLU_SAVED, false, false, a.value>(p, s);
+    });
+  return hipErrorInvalidValue;
+}
+
+}  // namespace fmlp

@@ -218,6 +218,90 @@ fmlp_status fmlp_glu_bwd(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf1
 size_t fmlp_glu_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
 
 /*
+ * The gated block with an 8-bit checkpoint
+ *
+ * fmlp_glu_bwd keeps nothing of the forward and recomputes g and u: two of its
+ * eight matrix products.  fmlp_glu_ckpt is fmlp_glu that also keeps g and u, in
+ * 8 bits (2.06 bytes a hidden unit and token, where bf16 would take 4), and
+ * fmlp_glu_ckpt_bwd is the backward pass that reads them: six products, and dm
+ * never leaves the registers.
+ *
+ *   codes  [M, 2H] OCP E4M3: g in columns [0, H), u in columns [H, 2H)
+ *   scales [M, 2 B] exponents, B = ceil(H / 32): g's blocks, then u's
+ *   value = e4m3(code) * 2^(scale - 127)
+ *
+ * A block is 32 consecutive hidden units of one row (the last one may be
+ * shorter).  Its exponent is the least one, at least -126, that brings the
+ * largest finite magnitude of the block to at most 448 (E4M3's largest); g and
+ * u are scaled by that power of two from the fp32 accumulators, which rounds
+ * nothing, and rounded once to E4M3 (nearest, ties to even): by at most 2^-4 of
+ * a value down to 2^-6 in the scaled unit, and 2^-10 in that unit below.  An
+ * infinity or a NaN does not enter the scale and is stored as NaN.  y is that
+ * of fmlp_glu's two-launch path: it does not see the 8 bits.
+ *
+ * The gradients are those of fmlp_glu_bwd's formulas at the stored g and u:
+ *   m = act(g) * u, dWd = dy^T m, dm = dy Wd, dg = dm * u * act'(g),
+ *   du = dm * act(g), dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x.
+ * m, dg and du are rounded to bf16 once before the product that consumes them;
+ * dm stays fp32.  Bitwise deterministic.  codes and scales are caller-owned and
+ * 16-byte aligned (fmlp_glu_ckpt_codes_size and fmlp_glu_ckpt_scales_size bytes); scales
+ * that the forward did not write must lie in [1, 254].  Shapes and errors as
+ * fmlp_glu and fmlp_glu_bwd (any M >= 0 runs the tiled GEMMs; fmlp_set_path does
+ * not apply; M == 0 writes zero weight gradients).  The workspaces
+ * need no initialisation and leave the first 8192 bytes (the decode header)
+ * alone.
+ */
+typedef uint8_t fmlp_fp8;  /* OCP FP8 E4M3 ("e4m3fn") code */
+
+fmlp_status fmlp_glu_ckpt(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf16* Wu, const fmlp_bf16* Wd,
+                          int gate_act, int64_t M, int64_t D, int64_t H, fmlp_bf16* y, fmlp_fp8* codes,
+                          uint8_t* scales, void* workspace, size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_glu_ckpt_workspace_size(int64_t M, int64_t D, int64_t H);
+size_t fmlp_glu_ckpt_codes_size(int64_t M, int64_t H);
+size_t fmlp_glu_ckpt_scales_size(int64_t M, int64_t H);
+fmlp_status fmlp_glu_ckpt_bwd(const fmlp_bf16* x, const fmlp_fp8* codes, const uint8_t* scales, const fmlp_bf16* Wg,
+                              const fmlp_bf16* Wu, const fmlp_bf16* Wd, int gate_act, const fmlp_bf16* dy, int64_t M,
+                              int64_t D, int64_t H, fmlp_bf16* dx, fmlp_bf16* dWg, fmlp_bf16* dWu, fmlp_bf16* dWd,
+                              void* workspace, size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_glu_ckpt_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
+
+/*
+ * Products grouped by expert
+ *
+ * The layer of fmlp_linear with a weight of its own for every group of rows
+ * (the projections of routed experts): rows [off[e], off[e+1]) of x [R, K] are
+ * group e's, and
+ *   y[r,:] = act(x[r,:] . W[e]^T + b[e]),   W [E,N,K], b [E,N] or NULL.
+ * group_off is a device array of E + 1 int32, off[0] >= 0, nondecreasing,
+ * off[E] <= R; it is read on the device only, so the sizes may come from a
+ * router on the same stream.  Groups may be empty and of any size.  Rows
+ * outside [off[0], off[E]) are not read, and their rows of y are left as they
+ * were.  A table that breaks these rules gives unspecified rows (offsets are
+ * clamped into [0, R] and to a running maximum): nothing outside the buffers is
+ * touched.  1 <= E <= 1024.  Accumulation in fp32, one rounding to bf16;
+ * deterministic: a row's result depends on its own group only.
+ *
+ * fmlp_grouped_linear_bwd gives the gradients for an upstream dy [R, N]:
+ *   dz = dy * act'(x W[e]^T + b[e]) (recomputed, rounded to bf16 once),
+ *   dx[r,:] = dz[r,:] W[e],  dW[e] = sum over e's rows of dz[r]^T x[r],
+ *   db[e] = sum of dz[r]  (db may be NULL).
+ * A group without rows gets dW[e] = 0 and db[e] = 0; rows of dx outside every
+ * group are left as they were.  R K, R N and N K must each be below 2^30
+ * (FMLP_E_SHAPE).  Both operands of dW and the weights of dx are read as
+ * stored.  Bitwise deterministic.
+ * Workspaces need no initialisation and leave the first 8192 bytes alone.
+ */
+fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W, const fmlp_bf16* b,
+                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, void* workspace,
+                                size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_grouped_linear_workspace_size(int32_t E);
+fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W,
+                                    const fmlp_bf16* b, int act, const fmlp_bf16* dy, int64_t R, int64_t K, int64_t N,
+                                    int32_t E, fmlp_bf16* dx, fmlp_bf16* dW, fmlp_bf16* db, void* workspace,
+                                    size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_grouped_linear_bwd_workspace_size(int64_t R, int64_t K, int64_t N, int32_t E, int act);
+
+/*
  * fmlp_glu without a workspace argument, for callers that cannot allocate
  * device memory (code under HIP graph capture, tight serving loops, harnesses
  * that forbid hipMalloc).  Same arguments, kernels, paths, results and errors
@@ -267,8 +351,6 @@ fmlp_status fmlp_glu_noalloc(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp
  * the launch-per-layer form.  The workspace: fmlp_w8_workspace_size bytes;
  * zero its header once, as for fmlp_mlp2.
  */
-typedef uint8_t fmlp_fp8;  /* OCP FP8 E4M3 ("e4m3fn") code */
-
 /* y[M,N] = act(x[M,K] . (w_scale[N] * e4m3(Wq[N,K]))^T + b[N]); b may be NULL. */
 fmlp_status fmlp_linear_w8(const fmlp_bf16* x, const fmlp_fp8* Wq, const float* w_scale,
                            const fmlp_bf16* b, int act, int64_t M, int64_t K, int64_t N,

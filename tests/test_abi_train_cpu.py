@@ -1,0 +1,118 @@
+"""The C ABI of the grouped products and of the gated block with an 8-bit
+checkpoint on the CPU: sizes, and every refusal before a device is touched."""
+import os
+
+import pytest
+
+OK, E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_WS = range(6)
+X, W, B, Y, WS, O, Q, S = (0x10000 * i for i in range(1, 9))   # fake, aligned, never dereferenced
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    import gemm_epilogue_bf16_amd as F
+
+    if not os.path.exists(F.library_path()):
+        from gemm_epilogue_bf16_amd.build import build
+
+        build()
+    return F.lib()
+
+
+def _err(L):
+    return L.fmlp_last_error().decode()
+
+
+def grouped(L, x=X, off=O, w=W, b=B, act=1, R=40, K=64, N=72, E=4, y=Y, ws=WS, nb=BIG):
+    return L.fmlp_grouped_linear(x, off, w, b, act, R, K, N, E, y, ws, nb, None)
+
+
+def grouped_bwd(L, x=X, off=O, w=W, b=B, act=1, dy=Y, R=40, K=64, N=72, E=4, dx=Y, dW=Y, db=B, ws=WS, nb=BIG):
+    return L.fmlp_grouped_linear_bwd(x, off, w, b, act, dy, R, K, N, E, dx, dW, db, ws, nb, None)
+
+
+COMMON = [
+    (dict(K=60), E_ALIGN, "K=60"), (dict(N=20), E_ALIGN, "N=20"), (dict(K=0), E_SHAPE, "K=0"),
+    (dict(N=1 << 22), E_SHAPE, "N=4194304"), (dict(R=-1), E_SHAPE, "R=-1"), (dict(R=1 << 31), E_SHAPE, "R=2147483648"),
+    (dict(E=0), E_ARG, "E=0"), (dict(E=1025), E_ARG, "E=1025"), (dict(act=5), E_ARG, "act=5"),
+    (dict(x=None), E_NULL, "x is NULL"), (dict(off=None), E_NULL, "group_off is NULL"), (dict(w=None), E_NULL, "W is NULL"),
+    (dict(x=X + 2), E_ALIGN, "x is not"), (dict(off=O + 2), E_ALIGN, "group_off is not 4-byte"),
+    (dict(b=B + 8), E_ALIGN, "b is not"), (dict(ws=None, nb=0), E_WS, "NULL"), (dict(nb=16), E_WS, "needs"),
+    (dict(ws=WS + 8), E_ALIGN, "workspace"),
+]
+
+
+@pytest.mark.parametrize("kw,status,msg", COMMON + [(dict(y=None), E_NULL, "y is NULL")])
+def test_grouped_validation(L, kw, status, msg):
+    assert grouped(L, **kw) == status and msg in _err(L)
+
+
+@pytest.mark.parametrize("kw,status,msg", COMMON + [
+    (dict(dy=None), E_NULL, "dy is NULL"), (dict(dx=None), E_NULL, "dx is NULL"), (dict(dW=None), E_NULL, "dW is NULL"),
+    (dict(db=B + 4), E_ALIGN, "db is not"),
+    (dict(R=1 << 20, K=1024), E_SHAPE, "2^30"), (dict(R=1 << 24, N=64), E_SHAPE, "2^30"),
+    (dict(K=32768, N=32768), E_SHAPE, "N*K=1073741824"),
+])
+def test_grouped_bwd_validation(L, kw, status, msg):
+    assert grouped_bwd(L, **kw) == status and msg in _err(L)
+
+
+def test_grouped_no_rows_is_a_noop(L):
+    assert grouped(L, x=None, R=0, y=None) == OK
+    assert grouped(L, x=None, R=0, y=None, w=None) == E_NULL
+
+
+def test_grouped_sizes(L):
+    plan = 8192 + 256 + 256 + 256   # header, two int32 tables and one int64 table of E + 1
+    assert L.fmlp_grouped_linear_workspace_size(4) == plan
+    assert L.fmlp_grouped_linear_workspace_size(0) == 0 and L.fmlp_grouped_linear_workspace_size(1025) == 0
+    assert L.fmlp_grouped_linear_workspace_size(1024) == 8192 + 2 * 4352 + 8448
+    assert L.fmlp_grouped_linear_bwd_workspace_size(40, 64, 72, 4, 0) == plan
+    assert L.fmlp_grouped_linear_bwd_workspace_size(40, 64, 72, 4, 1) == plan + 40 * 72 * 2 + 128   # dz
+    # 4 groups of one tile each over about 2048 rows: 4 parts of 512 rows
+    assert L.fmlp_grouped_linear_bwd_workspace_size(8192, 64, 72, 4, 0) == plan + 4 * 4 * 64 * 72 * 4
+    assert L.fmlp_grouped_linear_bwd_workspace_size(-1, 64, 72, 4, 0) == 0
+
+
+def ckpt(L, x=X, wg=W, wu=W, wd=W, act=4, M=20, D=64, H=72, y=Y, codes=Q, scales=S, ws=WS, nb=BIG):
+    return L.fmlp_glu_ckpt(x, wg, wu, wd, act, M, D, H, y, codes, scales, ws, nb, None)
+
+
+def ckpt_bwd(L, x=X, wg=W, wu=W, wd=W, act=4, M=20, D=64, H=72, codes=Q, scales=S, dy=Y, dx=Y, dWg=Y, dWu=Y, dWd=Y, ws=WS, nb=BIG):
+    return L.fmlp_glu_ckpt_bwd(x, codes, scales, wg, wu, wd, act, dy, M, D, H, dx, dWg, dWu, dWd, ws, nb, None)
+
+
+BLOCK = [
+    (dict(D=60), E_ALIGN, "D=60"), (dict(H=12), E_ALIGN, "H=12"), (dict(D=0), E_SHAPE, "D=0"), (dict(H=1 << 22), E_SHAPE, "H="),
+    (dict(M=-1), E_SHAPE, "M=-1"), (dict(act=9), E_ARG, "gate_act=9"), (dict(x=None), E_NULL, "x is NULL"),
+    (dict(wg=None), E_NULL, "Wg is NULL"), (dict(wu=None), E_NULL, "Wu is NULL"), (dict(wd=None), E_NULL, "Wd is NULL"),
+    (dict(codes=None), E_NULL, "codes is NULL"), (dict(scales=None), E_NULL, "scales is NULL"),
+    (dict(codes=Q + 8), E_ALIGN, "codes is not"), (dict(scales=S + 1), E_ALIGN, "scales is not"),
+    (dict(ws=None, nb=0), E_WS, "NULL"), (dict(nb=8192), E_WS, "needs"),
+]
+
+
+@pytest.mark.parametrize("kw,status,msg", BLOCK + [(dict(y=None), E_NULL, "y is NULL")])
+def test_ckpt_validation(L, kw, status, msg):
+    assert ckpt(L, **kw) == status and msg in _err(L)
+
+
+@pytest.mark.parametrize("kw,status,msg", BLOCK + [
+    (dict(dy=None), E_NULL, "dy is NULL"), (dict(dx=None), E_NULL, "dx is NULL"), (dict(dWg=None), E_NULL, "dWg is NULL"),
+    (dict(dWu=None), E_NULL, "dWu is NULL"), (dict(dWd=None), E_NULL, "dWd is NULL"),
+    (dict(M=1 << 22), E_SHAPE, "2^22"), (dict(H=1 << 21), E_SHAPE, "2H must"),
+])
+def test_ckpt_bwd_validation(L, kw, status, msg):
+    assert ckpt_bwd(L, **kw) == status and msg in _err(L)
+
+
+def test_ckpt_sizes_and_no_tokens(L):
+    assert L.fmlp_glu_ckpt_codes_size(20, 72) == 20 * 144
+    assert L.fmlp_glu_ckpt_scales_size(20, 72) == 20 * 2 * 3
+    assert L.fmlp_glu_ckpt_workspace_size(20, 64, 72) == 8192 + 3072
+    assert L.fmlp_glu_ckpt_bwd_workspace_size(0, 64, 72) > 8192
+    assert L.fmlp_glu_ckpt_codes_size(-1, 72) == 0 and L.fmlp_glu_ckpt_workspace_size(1, 0, 72) == 0
+    assert ckpt(L, M=0, x=None, y=None, codes=None, scales=None) == OK
+    # a checkpoint that is smaller than the recomputing backward's dm, and its workspace too
+    assert L.fmlp_glu_ckpt_bwd_workspace_size(4096, 4096, 14336) < L.fmlp_glu_bwd_workspace_size(4096, 4096, 14336)
