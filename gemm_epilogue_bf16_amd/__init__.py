@@ -19,6 +19,9 @@ raises.
     fmlp_linear_w8(x, Wq, s, b, act)               the same forms with FP8 E4M3 weights and a
     fmlp_mlp2_w8(x, W1q, s1, b1, W2q, s2, b2, act)  scale per output row, W = s[:, None] * e4m3(Wq);
     fmlp_glu_w8(x, Wgq, sg, Wuq, su, Wdq, sd, act)  decode only (at most 16 tokens)
+    fmlp_linear_w4(x, Wq, scales, zeros, b, act)    Linear and gated block with 4-bit weights, a scale (and a
+    fmlp_glu_w4(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, act)
+                                                    zero point) per 32, 64 or 128 k; at most 16 tokens
     fmlp_moe_route(x, Wr, top_k)                    -> (expert_ids, gate_w[, logits]): top_k of x Wr^T,
                                                        softmax over the chosen logits
 
@@ -71,6 +74,10 @@ __all__ = [
     "fmlp_linear_w8",
     "fmlp_mlp2_w8",
     "fmlp_glu_w8",
+    "fmlp_linear_w4",
+    "fmlp_glu_w4",
+    "bind_linear_w4",
+    "bind_glu_w4",
     "bind_linear_w8",
     "bind_mlp2_w8",
     "bind_glu_w8",
@@ -166,7 +173,11 @@ def lib() -> ctypes.CDLL:
                      ("fmlp_grouped_linear_bwd_workspace_size", [_i64] * 3 + [ctypes.c_int32, ctypes.c_int])):
             getattr(L, f).argtypes = a
             getattr(L, f).restype = _sz
-        for f in ("fmlp_glu_ckpt", "fmlp_glu_ckpt_bwd", "fmlp_grouped_linear", "fmlp_grouped_linear_bwd"):
+        L.fmlp_linear_w4.argtypes = [_p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p]
+        L.fmlp_glu_w4.argtypes = [_p] * 10 + [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _sz, _p]
+        L.fmlp_w4_workspace_size.argtypes = [_i64, _i64]
+        L.fmlp_w4_workspace_size.restype = _sz
+        for f in ("fmlp_linear_w4", "fmlp_glu_w4", "fmlp_glu_ckpt", "fmlp_glu_ckpt_bwd", "fmlp_grouped_linear", "fmlp_grouped_linear_bwd"):
             getattr(L, f).restype = ctypes.c_int
         L.fmlp_linear_w8.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p]
         L.fmlp_mlp2_w8.argtypes = [_p, _p, _p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _i64, _p, _p,
@@ -897,3 +908,78 @@ def bind_glu_w8(x, Wgq, sg, Wuq, su, Wdq, sd, gate_act: str = "gelu_tanh", out=N
                 workspace=None) -> BoundCall:
     with torch.cuda.device(x.device):
         return _glu_w8_call(x, Wgq, sg, Wuq, su, Wdq, sd, gate_act, out, workspace)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights with group scales, decode
+# ---------------------------------------------------------------------------
+def _w4_weight(name, q, s, z, N, K, x) -> int:
+    """Checks one 4-bit weight [N, K] and returns its group size."""
+    _dev_tensor(name, q, torch.uint8)
+    _dev_tensor(f"{name}'s scales", s)
+    _same_device(x, **{name: q, f"{name}'s scales": s})
+    if q.shape != (N, K // 2) or K % 2:
+        raise ValueError(f"{name} must be [{N}, {K // 2}] (two codes a byte), got {tuple(q.shape)}")
+    if s.dim() != 2 or s.shape[0] != N or s.shape[1] == 0 or K % s.shape[1]:
+        raise ValueError(f"{name}'s scales must be [{N}, {K} / group], got {tuple(s.shape)}")
+    if z is not None:
+        _dev_tensor(f"{name}'s zeros", z)
+        _same_device(x, **{f"{name}'s zeros": z})
+        if z.shape != s.shape:
+            raise ValueError(f"{name}'s zeros must be {tuple(s.shape)}, got {tuple(z.shape)}")
+    return K // s.shape[1]
+
+
+def _linear_w4_call(x, Wq, scales, zeros, b, act, out):
+    _dev_tensor("x", x)
+    K, N = x.shape[-1], Wq.shape[0]
+    G = _w4_weight("Wq", Wq, scales, zeros, N, K, x)
+    if b is not None:
+        _dev_tensor("b", b)
+        _same_device(x, b=b)
+        if b.shape != (N,):
+            raise ValueError(f"b must be [{N}], got {tuple(b.shape)}")
+    y = _out("out", out, x.shape[:-1] + (N,), x)
+    return BoundCall(lib().fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act],
+                                            x.numel() // K, K, N, G, y.data_ptr(), _stream(x.device)), y,
+                     (x, Wq, scales, zeros, b))
+
+
+def fmlp_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None):
+    """y = act(x W^T + b), W[n, k] = scales[n, k // G] * (code[n, k] - zeros[n, k // G]); x [..., K], at most 16 rows.
+
+    Wq uint8 [N, K / 2], code 2j in the low half of byte j; scales (and zeros, or None for 8) bf16 [N, K / G]."""
+    with torch.cuda.device(x.device):
+        return _linear_w4_call(x, Wq, scales, zeros, b, act, out)()
+
+
+def bind_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _linear_w4_call(x, Wq, scales, zeros, b, act, out)
+
+
+def _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace):
+    _dev_tensor("x", x)
+    D, H = x.shape[-1], Wgq.shape[0]
+    G = _w4_weight("Wgq", Wgq, sg, zg, H, D, x)
+    if _w4_weight("Wuq", Wuq, su, zu, H, D, x) != G or _w4_weight("Wdq", Wdq, sd, zd, D, H, x) != G:
+        raise ValueError("the three weights must have the same group size")
+    M = x.numel() // D
+    y = _out("out", out, x.shape, x)
+    L = lib()
+    ws = _scratch(x, workspace, L.fmlp_w4_workspace_size(M, H))
+    return BoundCall(L.fmlp_glu_w4, (x.data_ptr(), Wgq.data_ptr(), sg.data_ptr(), _ptr(zg), Wuq.data_ptr(), su.data_ptr(),
+                                     _ptr(zu), Wdq.data_ptr(), sd.data_ptr(), _ptr(zd), ACT[gate_act], M, D, H, G,
+                                     y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device)), y,
+                     (x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, ws))
+
+
+def fmlp_glu_w4(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act: str = "silu", out=None, workspace=None):
+    """fmlp_glu with 4-bit weights (Wgq, Wuq [H, D / 2], Wdq [D, H / 2], scales and zeros as for fmlp_linear_w4)."""
+    with torch.cuda.device(x.device):
+        return _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)()
+
+
+def bind_glu_w4(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act: str = "silu", out=None, workspace=None) -> BoundCall:
+    with torch.cuda.device(x.device):
+        return _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)

@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfmlp.so")
-SOURCES = ["abi.cpp", "train.cpp", "gemm.hip", "gemm_train.hip", "grouped.hip", "decode.hip", "decode_w8.hip", "small_mlp.hip", "moe.hip", "transpose.hip", "noalloc.hip",
+SOURCES = ["abi.cpp", "train.cpp", "serve.cpp", "decode_w4.hip", "gemm.hip", "gemm_train.hip", "grouped.hip", "decode.hip", "decode_w8.hip", "small_mlp.hip", "moe.hip", "transpose.hip", "noalloc.hip",
            "glu_fused.hip"]
 ARCH = "gfx950"
 # Per-source flags.  The GEMM main loop is written in issue order (fragment

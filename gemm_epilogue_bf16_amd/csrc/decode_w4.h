@@ -1,0 +1,32 @@
+// Launch interface of the 4-bit-weight decode kernel (decode_w4.hip).  Internal
+// to the library, like kernels.h; not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fmlp {
+
+// One decode layer (M <= 16 tokens) with 4-bit weights [N, K] and bf16 scales
+// (and zero points) [N, K / G]: W[n, k] = s (q - z), z = 8 where z0 is null;
+// G = 32, 64 or 128 and K % G == 0.  With q1 set it is the gate+up layer
+// y = act(x W0^T) * (x W1^T) (z0 and z1 both null or both set), else
+// y = act(x W0^T + bias).  One launch.
+struct W4Layer {
+  const uint16_t* x;     // [M, K] bf16
+  const uint8_t* q0;     // [N, K / 2], code 2j in the low half of byte j
+  const uint16_t* s0;    // [N, K / G] bf16
+  const uint16_t* z0;    // [N, K / G] bf16 or nullptr
+  const uint8_t* q1;     // gate+up: the up weights, or nullptr
+  const uint16_t* s1;
+  const uint16_t* z1;
+  const uint16_t* bias;  // [N] or nullptr (ungated only)
+  uint16_t* y;           // [M, N] bf16
+  int64_t K, N;
+  int G;
+  int act;               // Act; for a gated layer, the gate's activation
+};
+
+hipError_t launch_decode_w4(const W4Layer& L, int M, hipStream_t s);
+
+}  // namespace fmlp

@@ -1,0 +1,80 @@
+// C entry points of decode with 4-bit weights.  See include/fmlp.h for the
+// contract.
+#include "abi_calls.h"
+#include "decode_w4.h"
+
+using namespace fmlp;
+
+namespace {
+
+fmlp_status check_w4(int64_t M, int group) {
+  TRY(check_rows("M", M));
+  if (M > kDecodeMaxM)
+    return fail(FMLP_E_ARG, "4-bit-weight calls take M <= %lld tokens (M=%lld)", (long long)kDecodeMaxM, (long long)M);
+  if (group != 32 && group != 64 && group != 128) return fail(FMLP_E_ARG, "group=%d is not 32, 64 or 128", group);
+  return FMLP_OK;
+}
+
+fmlp_status check_w4_inner(const char* name, int64_t v, int group) {
+  TRY(check_inner(name, v));
+  if (v % group != 0) return fail(FMLP_E_ALIGN, "%s=%lld is not a multiple of the group size %d", name, (long long)v, group);
+  return FMLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf16* scales, const fmlp_bf16* zeros,
+                           const fmlp_bf16* b, int act, int64_t M, int64_t K, int64_t N, int group, fmlp_bf16* y,
+                           fmlp_stream stream) {
+  TRY(check_w4(M, group));
+  TRY(check_w4_inner("K", K, group));
+  TRY(check_inner("N", N));
+  TRY(check_act(act));
+  TOKEN_PTR(x, M);
+  REQUIRE_PTR(Wq);
+  REQUIRE_PTR(scales);
+  OPTIONAL_PTR(zeros);
+  OPTIONAL_PTR(b);
+  TOKEN_PTR(y, M);
+  if (M == 0) return ok();
+  TRY(check_device());
+  const W4Layer L{x, Wq, scales, zeros, nullptr, nullptr, nullptr, b, y, K, N, group, act};
+  return launched(launch_decode_w4(L, (int)M, static_cast<hipStream_t>(stream)), "linear (4-bit weights) launch");
+}
+
+size_t fmlp_w4_workspace_size(int64_t M, int64_t H) { return M <= 0 || H <= 0 ? 0 : kHeader + ws_bf16(M, H); }
+
+fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16* sg, const fmlp_bf16* zg,
+                        const uint8_t* Wuq, const fmlp_bf16* su, const fmlp_bf16* zu, const uint8_t* Wdq,
+                        const fmlp_bf16* sd, const fmlp_bf16* zd, int gate_act, int64_t M, int64_t D, int64_t H,
+                        int group, fmlp_bf16* y, void* workspace, size_t workspace_bytes, fmlp_stream stream) {
+  TRY(check_w4(M, group));
+  TRY(check_w4_inner("D", D, group));
+  TRY(check_w4_inner("H", H, group));
+  TRY(check_act(gate_act, "gate_act"));
+  TOKEN_PTR(x, M);
+  REQUIRE_PTR(Wgq);
+  REQUIRE_PTR(sg);
+  OPTIONAL_PTR(zg);
+  REQUIRE_PTR(Wuq);
+  REQUIRE_PTR(su);
+  OPTIONAL_PTR(zu);
+  REQUIRE_PTR(Wdq);
+  REQUIRE_PTR(sd);
+  OPTIONAL_PTR(zd);
+  if ((zg == nullptr) != (zu == nullptr)) return fail(FMLP_E_ARG, "zg and zu must both be given or both be NULL");
+  TOKEN_PTR(y, M);
+  TRY(check_workspace(workspace, workspace_bytes, fmlp_w4_workspace_size(M, H)));
+  if (M == 0) return ok();
+  TRY(check_device());
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint16_t* m = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kHeader);
+  const W4Layer L1{x, Wgq, sg, zg, Wuq, su, zu, nullptr, m, D, H, group, gate_act};
+  const W4Layer L2{m, Wdq, sd, zd, nullptr, nullptr, nullptr, nullptr, y, H, D, group, FMLP_ACT_NONE};
+  HIP_TRY(launch_decode_w4(L1, (int)M, s), "glu (4-bit weights) gate+up launch");
+  return launched(launch_decode_w4(L2, (int)M, s), "glu (4-bit weights) down launch");
+}
+
+}  // extern "C"

@@ -162,3 +162,27 @@ def check(name, got, want, bound):
         rel = float((got - want)[look].norm() / want[look].norm().clamp(min=1e-300))
         print(f"  {name}: rel {rel:.2e}, of its bound {float(((got - want).abs() / bound)[look].max()):.3f}", flush=True)
     assert worst <= 0, f"{name}: {int((off > 0).sum())} values outside their bound, worst by {worst:.3e}"
+
+
+def w4_dense(q, s, z):
+    """W and the magnitudes |s| (code + |z|) that its sums run over"""
+    c = torch.stack((q & 15, q >> 4), -1).reshape(q.shape[0], -1).double()
+    per = c.shape[1] // s.shape[1]
+    z = torch.full_like(s, 8.0).double() if z is None else z.double()
+    z, s = z.repeat_interleave(per, 1), s.double().repeat_interleave(per, 1)
+    return s * (c - z), s.abs() * (c + z.abs())
+
+
+def w4_linear(x, ex, q, s, z):
+    """x W^T and its error: fp32 sums of x code and of -x z, and one scale each"""
+    W, mag = w4_dense(q, s, z)
+    e = 2 * (x.shape[1] + 16) * F32 * (x.abs() @ mag.t())
+    return x @ W.t(), e if ex is None else e + ex @ W.abs().t()
+
+
+def w4_glu(x, wg, wu, wd, act):
+    (g, eg), (u, eu) = w4_linear(x, None, *wg), w4_linear(x, None, *wu)
+    a = act64(g, act)[0]
+    m, em = prod(a, act_err(g, eg, act)[0], u, eu)
+    y, e = w4_linear(m, rounded(m, em), *wd)
+    return y, rounded(y, e)

@@ -116,3 +116,40 @@ def test_ckpt_sizes_and_no_tokens(L):
     assert ckpt(L, M=0, x=None, y=None, codes=None, scales=None) == OK
     # a checkpoint that is smaller than the recomputing backward's dm, and its workspace too
     assert L.fmlp_glu_ckpt_bwd_workspace_size(4096, 4096, 14336) < L.fmlp_glu_bwd_workspace_size(4096, 4096, 14336)
+
+
+def w4(L, x=X, q=Q, s=S, z=B, b=B, act=4, M=4, K=256, N=72, g=64, y=Y):
+    return L.fmlp_linear_w4(x, q, s, z, b, act, M, K, N, g, y, None)
+
+
+def glu_w4(L, x=X, q=Q, s=S, zg=B, zu=B, zd=B, act=4, M=4, D=256, H=128, g=64, y=Y, ws=WS, nb=BIG):
+    return L.fmlp_glu_w4(x, q, s, zg, q, s, zu, q, s, zd, act, M, D, H, g, y, ws, nb, None)
+
+
+FOUR = [
+    (dict(M=17), E_ARG, "M=17"), (dict(M=-1), E_SHAPE, "M=-1"), (dict(g=16), E_ARG, "group=16"), (dict(g=0), E_ARG, "group=0"),
+    (dict(g=-32), E_ARG, "group=-32"), (dict(act=5), E_ARG, "act=5"), (dict(x=None), E_NULL, "x is NULL"),
+    (dict(q=None), E_NULL, "q is NULL"), (dict(s=None), E_NULL, " is NULL"), (dict(y=None), E_NULL, "y is NULL"),
+    (dict(q=Q + 8), E_ALIGN, "q is not"), (dict(s=S + 2), E_ALIGN, "is not 16-byte"),
+]
+
+
+@pytest.mark.parametrize("kw,status,msg", FOUR + [
+    (dict(K=288), E_ALIGN, "K=288"), (dict(K=0), E_SHAPE, "K=0"), (dict(N=20), E_ALIGN, "N=20"), (dict(N=1 << 22), E_SHAPE, "N="),
+    (dict(z=B + 8), E_ALIGN, "zeros is not"), (dict(b=B + 8), E_ALIGN, "b is not")])
+def test_linear_w4_validation(L, kw, status, msg):
+    assert w4(L, **kw) == status and msg in _err(L)
+
+
+@pytest.mark.parametrize("kw,status,msg", FOUR + [
+    (dict(D=288), E_ALIGN, "D=288"), (dict(H=96), E_ALIGN, "H=96"), (dict(zg=None), E_ARG, "zg and zu"), (dict(zu=None), E_ARG, "zg and zu"),
+    (dict(zd=B + 8), E_ALIGN, "zd is not"), (dict(ws=None, nb=0), E_WS, "NULL"), (dict(nb=8192), E_WS, "needs")])
+def test_glu_w4_validation(L, kw, status, msg):
+    assert glu_w4(L, **kw) == status and msg in _err(L)
+
+
+def test_w4_sizes_and_no_tokens(L):
+    assert L.fmlp_w4_workspace_size(4, 128) == 8192 + 1024 and L.fmlp_w4_workspace_size(0, 128) == 0
+    assert w4(L, M=0, x=None, y=None) == OK
+    assert glu_w4(L, M=0, x=None, y=None, ws=None, nb=0) == OK
+    assert w4(L, M=0, x=None, y=None, q=None) == E_NULL
