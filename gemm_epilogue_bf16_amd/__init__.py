@@ -173,10 +173,12 @@ def lib() -> ctypes.CDLL:
                      ("fmlp_grouped_linear_bwd_workspace_size", [_i64] * 3 + [ctypes.c_int32, ctypes.c_int])):
             getattr(L, f).argtypes = a
             getattr(L, f).restype = _sz
-        L.fmlp_linear_w4.argtypes = [_p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p]
+        L.fmlp_linear_w4.argtypes = [_p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _sz, _p]
         L.fmlp_glu_w4.argtypes = [_p] * 10 + [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _sz, _p]
-        L.fmlp_w4_workspace_size.argtypes = [_i64, _i64]
-        L.fmlp_w4_workspace_size.restype = _sz
+        L.fmlp_linear_w4_workspace_size.argtypes = [_i64, _i64, ctypes.c_int]
+        L.fmlp_linear_w4_workspace_size.restype = _sz
+        L.fmlp_glu_w4_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+        L.fmlp_glu_w4_workspace_size.restype = _sz
         for f in ("fmlp_linear_w4", "fmlp_glu_w4", "fmlp_glu_ckpt", "fmlp_glu_ckpt_bwd", "fmlp_grouped_linear", "fmlp_grouped_linear_bwd"):
             getattr(L, f).restype = ctypes.c_int
         L.fmlp_linear_w8.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p]
@@ -930,7 +932,7 @@ def _w4_weight(name, q, s, z, N, K, x) -> int:
     return K // s.shape[1]
 
 
-def _linear_w4_call(x, Wq, scales, zeros, b, act, out):
+def _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace):
     _dev_tensor("x", x)
     K, N = x.shape[-1], Wq.shape[0]
     G = _w4_weight("Wq", Wq, scales, zeros, N, K, x)
@@ -940,22 +942,26 @@ def _linear_w4_call(x, Wq, scales, zeros, b, act, out):
         if b.shape != (N,):
             raise ValueError(f"b must be [{N}], got {tuple(b.shape)}")
     y = _out("out", out, x.shape[:-1] + (N,), x)
-    return BoundCall(lib().fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act],
-                                            x.numel() // K, K, N, G, y.data_ptr(), _stream(x.device)), y,
-                     (x, Wq, scales, zeros, b))
+    L = lib()
+    M = x.numel() // K
+    need = L.fmlp_linear_w4_workspace_size(M, K, G)
+    ws = _scratch(x, workspace, need) if need else None
+    return BoundCall(L.fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act],
+                                        M, K, N, G, y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                        _stream(x.device)), y, (x, Wq, scales, zeros, b, ws))
 
 
-def fmlp_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None):
+def fmlp_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None, workspace=None):
     """y = act(x W^T + b), W[n, k] = scales[n, k // G] * (code[n, k] - zeros[n, k // G]); x [..., K], at most 16 rows.
 
     Wq uint8 [N, K / 2], code 2j in the low half of byte j; scales (and zeros, or None for 8) bf16 [N, K / G]."""
     with torch.cuda.device(x.device):
-        return _linear_w4_call(x, Wq, scales, zeros, b, act, out)()
+        return _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace)()
 
 
-def bind_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None) -> BoundCall:
+def bind_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None, workspace=None) -> BoundCall:
     with torch.cuda.device(x.device):
-        return _linear_w4_call(x, Wq, scales, zeros, b, act, out)
+        return _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace)
 
 
 def _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace):
@@ -967,7 +973,7 @@ def _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, worksp
     M = x.numel() // D
     y = _out("out", out, x.shape, x)
     L = lib()
-    ws = _scratch(x, workspace, L.fmlp_w4_workspace_size(M, H))
+    ws = _scratch(x, workspace, L.fmlp_glu_w4_workspace_size(M, D, H, G))
     return BoundCall(L.fmlp_glu_w4, (x.data_ptr(), Wgq.data_ptr(), sg.data_ptr(), _ptr(zg), Wuq.data_ptr(), su.data_ptr(),
                                      _ptr(zu), Wdq.data_ptr(), sd.data_ptr(), _ptr(zd), ACT[gate_act], M, D, H, G,
                                      y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device)), y,

@@ -8,32 +8,51 @@
 // points).
 //
 // Arithmetic.  A byte 0x0q read as E4M3 is q * 2^-9 for every q (codes below 8
-// are its subnormals, 8 .. 15 its first binade), so the hardware's scaled
-// conversion with 2^9 turns two codes at a time into the bf16 integers q,
-// exactly.  Within a group
-//   sum_k x (q - z) = sum_k x q + sum_k x (-z),
-// both on v_mfma_f32_16x16x32_bf16 into one fp32 accumulator (the second with a
-// constant weight operand; without zero points it is the same for every weight
-// row and computed once); the group's scale multiplies the finished sum, in
-// fp32.  Nothing is rounded to fewer bits before the output's bf16.  A token
-// that holds an infinity or a NaN gets NaN or infinite outputs; others do not
-// see it (tokens are rows of the matrix product).
+// are its subnormals, 8 .. 15 its first binade), so a mask and a shift turn 8
+// codes into 8 matrix operands, with nothing to convert.  The activations meet
+// them as a sum of two E4M3 values: of a token's 128 k ("a chunk"), 2^e is the
+// least power of two that brings the largest magnitude to 448 or less, and
+//   x = 2^e hi + 2^(e-4) lo,  hi = e4m3(x 2^-e),  lo = e4m3(16 (x 2^-e - hi)).
+// A bf16 has 8 significant bits and hi and lo take 4 each, so this is exact for
+// every x within 14 binades of the chunk's largest, and off by at most 2^-21 of
+// that largest below.  v_mfma_scale_f32_16x16x128_f8f6f4 multiplies a whole
+// chunk, with 2^e and 2^9 as its block scales.  (bf16 operands need four
+// 16x16x32 MFMAs and a conversion of every code: 97 ns and 134 ns a KB of codes
+// and SIMD, against 17 or 33 ns and about 50 ns, and made the kernel compute
+// bound.)  The instruction adds its 128 products and the accumulator in fp32,
+// but was seen to align neighbouring products before that to 13 bits below the
+// larger one: a relative 2^-13 of a product, where the output rounds at 2^-9.
+//   sum_k x (q - z) = sum_k x q - z sum_k x,
+// the second sum in fp32 once per token and group.  The group's scale multiplies
+// the finished sum in fp32.  A token that holds an infinity or a NaN gets NaN;
+// others do not see it (tokens are rows of the matrix product).
+//
+// Groups smaller than a chunk.  The MFMA sums over 128 k; with G = 64 or 32 it
+// runs 2 or 4 times, each with the block scales of the other groups at 2^-127
+// on both operands (their products underflow).  A block of the instruction is
+// half of the registers of two lane groups, so with G = 32 two words change
+// places between neighbouring lane groups first (permlane16_swap).
 //
 // Layout.  The activations are the MFMA's row operand and 16 weight rows its
-// column operand, so a lane's four results are four tokens of ONE weight row
-// and need one scale.  A 16-byte load gives a lane 32 consecutive codes of its
-// row and the wave 128 codes ("a chunk") of 16 rows.  With G = 128 the four
-// words of a lane feed four MFMAs as they are: the contraction is order-free
-// within a group.  With G = 32 or 64 an MFMA's 32 k must be consecutive, and
-// four half-wave swaps (permlane32 / permlane16) exchange words between the
-// four lanes of a row.  8 waves share a block's rows and split k in runs of U
-// chunks; partial sums meet in LDS in wave order (deterministic).  Weight
-// batches are double-buffered in registers.
+// column operand, so a lane's four results are four rows of ONE weight row and
+// need one scale.  Up to 8 tokens, rows 0-7 are their hi and 8-15 their lo parts
+// and one MFMA does both (the two results of a token are added at the end, and
+// each carries half of the zero point's sum); beyond, a second MFMA takes lo.
+// A 16-byte load gives a lane 32 consecutive codes of its row.
 //
-// Activations: up to 64 KB of them are staged in LDS once per block (16 weight
-// rows a block); a larger set is read from L2 beside the weights, where a
-// block takes twice the rows so that half of those reads serve.  Every token's
-// row of the operand is independent, so rows past M need no masking.
+// A block's 8 waves are WR row tiles (16 rows each, gate and up rows for a
+// gated layer) times WK parts of k.  The grid is persistent (two blocks a CU)
+// and a block's work is one stream of steps (U chunks per wave) through its
+// tiles, double-buffered in registers: the next tile's first weights are in
+// flight while a tile is finished.  Partial sums of the WK waves meet in LDS
+// in wave order (deterministic).
+//
+// Activations in LDS are records, one per chunk: hi and lo of every token in
+// operand order, their exponents, and the groups' sums.  Up to 64 KB of them a
+// block makes its own from x once, while its first weights are in flight.
+// Larger sets are made once per call by a small kernel into the workspace and
+// stream through LDS with the weights, a step at a time (1 KB pieces by loads
+// that write LDS, two buffers, one barrier a step).
 #include <algorithm>
 
 #include "common.h"
@@ -59,42 +78,113 @@ __device__ __forceinline__ u32x4_t load16_stream(__amdgpu_buffer_rsrc_t d, uint3
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(d, (int)off, 0, 2));
 }
 
-// words w[i] of lane group g -> w[g] of lane group i (4 x 4 over the 16-lane groups)
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void exchange_words(uint32_t w[4]) {
-  swap32(w[0], w[2]);
-  swap32(w[1], w[3]);
-  swap16(w[0], w[1]);
-  swap16(w[2], w[3]);
-}
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// 8 codes of a word -> 8 bf16 integers, in k order
-__device__ __forceinline__ u32x4_t expand(uint32_t w) {
-  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;   // even codes, odd codes
-  const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u);      // codes 0 1 2 3
-  const uint32_t b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);      // codes 4 5 6 7
-  u32x4_t r;
-  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false));
-  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true));
-  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false));
-  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true));
+// ---------------------------------------------------------------------------
+// Records: one per chunk.  Operand bytes of 2 M slots (token m's hi in slot m, lo
+// in slot M + m) as [half][lane group][slot][16], the slots' exponents (+ 127,
+// one byte each), then [group][tokens] fp32 sums.
+// ---------------------------------------------------------------------------
+struct Record {
+  int slots, exps, sums, tokens, bytes;
+};
+__host__ __device__ __forceinline__ Record record_of(int M, int gs) {
+  Record r;
+  r.slots = 2 * M;
+  r.exps = r.slots * 128;
+  r.sums = r.exps + (M <= 8 ? 16 : 32);
+  r.tokens = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  r.bytes = r.sums + (kChunk >> gs) * r.tokens * 4;
   return r;
 }
 
-// one bf16 in all 8 places of an operand, sign flipped
-__device__ __forceinline__ u32x4_t minus_all(uint32_t bf) {
-  const uint32_t v = (bf | (bf << 16)) ^ 0x80008000u;
-  u32x4_t r;
-  r[0] = r[1] = r[2] = r[3] = v;
+// 16 lanes (i = 0 .. 15) put one token's chunk into its record: lane i has k
+// 8 i .. 8 i + 7 (zeros past K).
+template <int GS, bool ZEROS>
+__device__ __forceinline__ void put_record(uint8_t* rec, const Record& R, const u32x4_t& xv, int m, int M, int i) {
+  float v[8];
+  unpack_bf16x8(xv, v);
+  float top = 0.f, sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = fabsf(v[j]);
+    top = fmaxf(top, a < __builtin_inff() ? a : 0.f);
+    sum += v[j];
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+#pragma unroll
+  for (int d = 1; d < (1 << GS) / 8; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  const uint32_t bits = __float_as_uint(top);
+  // at least -122: the lo part's exponent byte stays positive
+  const int e = max((int)(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), -122);
+  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t hi[2], lo[2];   // even k, odd k: the order of a word's low and high halves
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    float a[4], h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = v[2 * j + o] * inv;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a[0], a[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], w, true);
+    hi[o] = (uint32_t)w;
+    const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    h[0] = h0[0];
+    h[1] = h0[1];
+    h[2] = h1[0];
+    h[3] = h1[1];
+    int l = __builtin_amdgcn_cvt_pk_fp8_f32(16.f * (a[0] - h[0]), 16.f * (a[1] - h[1]), 0, false);
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(16.f * (a[2] - h[2]), 16.f * (a[3] - h[3]), l, true);
+    lo[o] = (uint32_t)l;
+  }
+  // word d of lane group g of the weights: its place in the operand
+  const int g = i >> 2, d = i & 3;
+  const int half = GS == 5 ? g & 1 : d >> 1;
+  const int lg = GS == 5 ? (g & 2) | (d >> 1) : g;
+  uint8_t* at = rec + (half * 4 + lg) * (R.slots * 16) + (d & 1) * 8;
+  *reinterpret_cast<uint2*>(at + m * 16) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(at + (M + m) * 16) = make_uint2(lo[0], lo[1]);
+  if (i == 0) {
+    rec[R.exps + m] = (uint8_t)(e + 127);
+    rec[R.exps + M + m] = (uint8_t)(e + 123);
+  }
+  constexpr int kPer = (1 << GS) / 8;   // lanes of a group
+  if (i % kPer == 0)
+    reinterpret_cast<float*>(rec + R.sums)[(i / kPer) * R.tokens + m] = (ZEROS ? -1.f : -8.f) * (M <= 8 ? 0.5f : 1.f) * sum;
+}
+
+constexpr int kPutThreads = 256;
+template <int GS, bool ZEROS>
+__global__ __launch_bounds__(kPutThreads) void w4_records_kernel(const uint16_t* x, int M, int K, int chunks,
+                                                                 uint8_t* out) {
+  const int u = blockIdx.x * (kPutThreads / 16) + (threadIdx.x >> 4);   // chunk u / M, token u % M
+  const int i = threadIdx.x & 15;
+  if (u >= M * chunks) return;   // 16 lanes together
+  const Record R = record_of(M, GS);
+  const int c = u / M, m = u - c * M;
+  const int k = c * kChunk + i * 8;
+  put_record<GS, ZEROS>(out + (int64_t)c * R.bytes, R, k < K ? ld16(x + (int64_t)m * K + k) : zero4(), m, M, i);
+}
+
+// the 32 codes of a lane's 4 words as operand bytes, words 0 and 1 in the first
+// half of the registers (G = 32: neighbouring lane groups exchange words first)
+template <int GS>
+__device__ __forceinline__ i32x8_t expand(const u32x4_t& q) {
+  uint32_t w[4] = {q[0], q[1], q[2], q[3]};
+  if constexpr (GS == 5) {
+    const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
+    w[0] = a[0];
+    w[2] = a[1];
+    w[1] = b[0];
+    w[3] = b[1];
+  }
+  i32x8_t r;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    r[2 * d] = (int)(w[d] & 0x0F0F0F0Fu);
+    r[2 * d + 1] = (int)((w[d] >> 4) & 0x0F0F0F0Fu);
+  }
   return r;
 }
 
@@ -104,6 +194,7 @@ __device__ __forceinline__ u32x4_t minus_all(uint32_t bf) {
 template <int NV, bool WHOLE>
 struct Values {
   static constexpr int kWords = WHOLE ? (NV + 1) / 2 : NV;
+  static constexpr int kLoads = !WHOLE ? NV : NV <= 8 ? 1 : NV / 8;
   uint32_t v[kWords];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t off, int have) {
     if constexpr (!WHOLE) {
@@ -140,79 +231,73 @@ struct Values {
   }
 };
 
-// NS weight streams (row tiles, gate and up), U chunks each
-template <int NS, int U, int NV, bool WHOLE, bool ZEROS, bool XL>
+// NS weight streams (gate and up), U chunks each
+template <int NS, int U, int NV, bool WHOLE, bool ZEROS>
 struct Batch {
   u32x4_t w[NS][U];
   Values<NV, WHOLE> s[NS];
   Values<ZEROS ? NV : 2, WHOLE> z[ZEROS ? NS : 1];
-  u32x4_t x[XL ? 1 : U][4];
 };
 
-// GS: log2 of the group size.  WHOLE: K is a multiple of U chunks, so no load
-// needs a mask and scales come as aligned vectors.  XL: activations in LDS.
-template <bool DUAL, int RT, int U, int GS, bool ZEROS, bool WHOLE, bool XL>
-__global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M) {
-  constexpr int SETS = DUAL ? 2 : 1;
-  constexpr int NS = RT * SETS;            // stream s: row tile s / SETS, set s % SETS
+// GS: log2 of the group size.  WHOLE: K is a multiple of U chunks, so a step
+// exists in full or not at all and scales come as aligned vectors.  XL: all
+// records in LDS, made here.  M8: at most 8 tokens.
+template <bool DUAL, int WR, int U, int GS, bool ZEROS, bool WHOLE, bool XL, bool M8>
+__global__ __launch_bounds__(kThreads, 4) void decode_w4_kernel(W4Layer L, int M) {
+  constexpr int NS = DUAL ? 2 : 1;
+  constexpr int WK = kWaves / WR;
   constexpr int GPC = kChunk >> GS;        // groups per chunk
-  constexpr int IPG = 4 / GPC;             // MFMAs per group
-  constexpr int NV = U * GPC;              // scales of a batch
-  constexpr bool FINE = GPC > 1;
-  using B = Batch<NS, U, NV, WHOLE, ZEROS, XL>;
+  constexpr int NV = U * GPC;              // scales of a step
+  constexpr int SC = WK * U;               // chunks of a block's step
+  using B = Batch<NS, U, NV, WHOLE, ZEROS>;
+  // load instructions of a step's weights, scales and zero points
+  constexpr int kLoads = NS * (U + (ZEROS ? 2 : 1) * Values<NV, WHOLE>::kLoads);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15;   // weight row of a tile; token of the activation operand
+  const int wr = wave / WK, wk = wave % WK;
+  const int r = lane & 15;   // weight row of a tile; row of the activation operand
   const int g = lane >> 4;
   const int K = (int)L.K;
   const int groups = K >> GS;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-  const int rows = (int)min<int64_t>(16 * RT, L.N - n0);
   const int chunks = (K + kChunk - 1) / kChunk;
-  const int nb = (chunks + kWaves * U - 1) / (kWaves * U);   // batches of the first wave
+  const int steps = (chunks + SC - 1) / SC;   // of a tile
+  const int tiles = (int)((L.N + 16 * WR - 1) / (16 * WR));
+  const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // grid <= tiles
+  const int total = mine * steps;
+  const Record R = record_of(M, GS);
 
-  __amdgpu_buffer_rsrc_t dw[SETS], ds[SETS], dz[SETS];
-#pragma unroll
-  for (int t = 0; t < SETS; ++t) {
-    dw[t] = w4_desc((t ? L.q1 : L.q0) + n0 * (K / 2), (uint32_t)rows * (uint32_t)(K / 2));
-    ds[t] = w4_desc((t ? L.s1 : L.s0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u);
-    if constexpr (ZEROS) dz[t] = w4_desc((t ? L.z1 : L.z0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u);
-  }
-  const __amdgpu_buffer_rsrc_t dx = w4_desc(L.x, (uint32_t)(M * K) * 2u);
-  // codes 32 g .. of a chunk; the MFMA's k of lane group g: 8 g .. (FINE) or 32 g ..
   const uint32_t wlane = (uint32_t)(r * (K / 2) + g * 16);
   const uint32_t slane = (uint32_t)(r * groups) * 2u;
-  const int xk = FINE ? 8 * g : 32 * g;
-  constexpr int kXStep = FINE ? 32 : 8;   // k between an operand's four MFMAs
-  const int xstride = 2 * (chunks * kChunk) + 16;   // bytes of a staged row; + 16: rows in different banks
-  const uint8_t* xl = lds + (r < M ? r : 0) * xstride + 2 * xk;
-  const uint32_t xg = r < M ? (uint32_t)(r * K + xk) * 2u : kOutOfRange;
+  constexpr int kRed = kWaves * NS * 64 * 16;   // the partial sums of a tile
+  const int xbuf = XL ? chunks * R.bytes : max((SC * R.bytes + 1023) / 1024 * 1024, kRed);   // an activation buffer
+  // the lane's slot (rows without a token read slot 0; their results are not used)
+  const int slot = M8 ? ((r & 7) < M ? (r & 7) + (r >> 3) * M : 0) : (r < M ? r : 0);
+  const int xop = g * (R.slots * 16) + slot * 16;    // the lane's operand bytes in a record, first half
+  const int xsum = R.sums + 16 * (M8 ? (R.tokens == 8 ? g & 1 : 0) : g);   // the sums of its 4 result rows' tokens
 
-  auto issue = [&](B& b, int i) {
-    const int c0 = (i * kWaves + wave) * U;
+  int it = blockIdx.x, is = 0;   // tile and step of the next weights issued
+  auto issue = [&](B& b) {
+    const int64_t n0 = ((int64_t)it * WR + wr) * 16;
+    const int rows = (int)max<int64_t>(min<int64_t>(16, L.N - n0), 0);
+    const int c0 = (is * WK + wk) * U;
+    const bool any = c0 < chunks;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint32_t row = (uint32_t)((s / SETS) * 16);
-      const int left = WHOLE ? U : chunks - c0;   // chunks from c0 on
+      const __amdgpu_buffer_rsrc_t dw = w4_desc((s ? L.q1 : L.q0) + n0 * (K / 2), (uint32_t)rows * (uint32_t)(K / 2));
+      const __amdgpu_buffer_rsrc_t ds = w4_desc((s ? L.s1 : L.s0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u);
+      const uint32_t wo = wlane + (any ? (uint32_t)c0 * 64u : kOutOfRange);
 #pragma unroll
-      for (int j = 0; j < U; ++j)
-        b.w[s][j] = load16_stream(dw[s % SETS],
-                                  WHOLE || j < left ? wlane + row * (uint32_t)(K / 2) + (uint32_t)(c0 + j) * 64u : kOutOfRange);
-      const uint32_t so = slane + row * (uint32_t)groups * 2u + (uint32_t)(c0 * GPC) * 2u;
-      const int have = WHOLE ? NV : groups - c0 * GPC;
-      b.s[s].load(ds[s % SETS], so, have);
-      if constexpr (ZEROS) b.z[s].load(dz[s % SETS], so, have);
+      for (int j = 0; j < U; ++j) b.w[s][j] = load16_stream(dw, WHOLE || c0 + j < chunks ? wo + 64u * j : kOutOfRange);
+      const uint32_t so = slane + (any ? (uint32_t)(c0 * GPC) * 2u : kOutOfRange);
+      b.s[s].load(ds, so, groups - c0 * GPC);
+      if constexpr (ZEROS)
+        b.z[s].load(w4_desc((s ? L.z1 : L.z0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u), so, groups - c0 * GPC);
     }
-    if constexpr (!XL) {
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int k = (c0 + j) * kChunk + kXStep * q;
-          b.x[j][q] = load16(dx, WHOLE || k + xk < K ? xg + (uint32_t)k * 2u : kOutOfRange);
-        }
+    if (++is == steps) {
+      is = 0;
+      it += gridDim.x;
     }
   };
   auto hold = [&](B& b) {
@@ -223,181 +308,251 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M) {
       b.s[s].hold();
       if constexpr (ZEROS) b.z[s].hold();
     }
-    if constexpr (!XL) {
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(b.x[j][q]));
-    }
   };
+  // the records of a step into the LDS buffer at `base`, 1 KB per instruction
+  const i32x4_t xd = make_desc(reinterpret_cast<uint64_t>(L.records), (uint32_t)(XL ? 0 : chunks * R.bytes));
+  auto stage_x = [&](uint32_t base, int step) {
+    const int off = step * SC * R.bytes;
+    const int pieces = (SC * R.bytes + 1023) / 1024;
+    for (int t = wave; t < pieces; t += kWaves)   // wave-uniform
+      asm_load_lds(xd, uniform32(base + (uint32_t)(t * 1024)), (uint32_t)(off + t * 1024 + lane * 16));
+  };
+  const uint32_t xlds = lds_addr(lds);
+
   f32x4_t tot[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) tot[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const u32x4_t minus8 = minus_all(0x4100u);
-
-  auto consume = [&](const B& b, int i) {
-    const int c0 = (i * kWaves + wave) * U;
+  // block scales of the weights: 2^9 where the lane's block belongs to group t
+  int bscale[GPC];
+  bool mine_t[GPC];
+#pragma unroll
+  for (int t = 0; t < GPC; ++t) {
+    mine_t[t] = GS == 7 || (GS == 6 ? (g & 1) == t : g == (t & 1) * 2 + (t >> 1));
+    bscale[t] = mine_t[t] ? 136 : 0;
+  }
+  auto operand = [&](const uint8_t* rec, int at) {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(rec + at);
+    const u32x4_t b = *reinterpret_cast<const u32x4_t*>(rec + at + 4 * (R.slots * 16));
+    i32x8_t v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = (int)a[j];
+      v[4 + j] = (int)b[j];
+    }
+    return v;
+  };
+  auto consume = [&](const B& b, int step, int buf) {
+    const int c0 = (step * WK + wk) * U;
+    const uint8_t* recs = lds + (XL ? c0 * R.bytes : buf * xbuf + wk * U * R.bytes);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if (!WHOLE && c0 + j >= chunks) break;   // wave-uniform
-      u32x4_t x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        x[q] = XL ? *reinterpret_cast<const u32x4_t*>(xl + (c0 + j) * (2 * kChunk) + 2 * kXStep * q) : b.x[XL ? 0 : j][q];
-      f32x4_t corr[GPC];
-      if constexpr (!ZEROS) {
-#pragma unroll
-        for (int t = 0; t < GPC; ++t) {
-          corr[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < IPG; ++q) corr[t] = mfma_16x16x32(x[t * IPG + q], minus8, corr[t]);
-        }
-      }
+      if (WHOLE ? c0 >= chunks : c0 + j >= chunks) break;   // wave-uniform
+      const uint8_t* rec = recs + j * R.bytes;
+      const i32x8_t xh = operand(rec, xop);
+      const int eh = rec[R.exps + slot];
+      i32x8_t xl;
+      if constexpr (!M8) xl = operand(rec, xop + M * 16);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        uint32_t w[4] = {b.w[s][j][0], b.w[s][j][1], b.w[s][j][2], b.w[s][j][3]};
-        if constexpr (FINE) exchange_words(w);
+        const i32x8_t w = expand<GS>(b.w[s][j]);
+        f32x4_t acc[GPC];
 #pragma unroll
         for (int t = 0; t < GPC; ++t) {
-          f32x4_t acc;
+          const f32x4_t sums = *reinterpret_cast<const f32x4_t*>(rec + xsum + t * (R.tokens * 4));
+          const int ea = mine_t[t] ? eh : 0;
           if constexpr (ZEROS) {
-            acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            const u32x4_t z = minus_all(b.z[s].bits(j * GPC + t));
+            const float z = b.z[s].f32(j * GPC + t);
 #pragma unroll
-            for (int q = 0; q < IPG; ++q) acc = mfma_16x16x32(x[t * IPG + q], z, acc);
+            for (int v = 0; v < 4; ++v) acc[t][v] = z * sums[v];
           } else {
-            acc = corr[t];
+            acc[t] = sums;
           }
+          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xh, w, acc[t], 0, 0, 0, ea, 0, bscale[t]);
+          if constexpr (!M8) {
+            const int el = mine_t[t] ? eh - 4 : 0;
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xl, w, acc[t], 0, 0, 0, el, 0, bscale[t]);
+          }
+        }
 #pragma unroll
-          for (int q = 0; q < IPG; ++q) acc = mfma_16x16x32(x[t * IPG + q], expand(w[t * IPG + q]), acc);
+        for (int t = 0; t < GPC; ++t) {
           const float sc = b.s[s].f32(j * GPC + t);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) tot[s][v] = fmaf(sc, acc[v], tot[s][v]);
+          for (int v = 0; v < 4; ++v) tot[s][v] = fmaf(sc, acc[t][v], tot[s][v]);
         }
       }
     }
   };
-
-  // this wave's batches: those whose first chunk exists
-  int mine = 0;
-  if (wave * U < chunks) mine = (chunks - wave * U + kWaves * U - 1) / (kWaves * U);
-  (void)nb;
-  B A, C;
-  if (mine > 0) issue(A, 0);
-  if constexpr (XL) {
-    // rows of x straight into LDS, 1 KB per instruction, all in flight before
-    // one wait; zeros behind a row whose K ends inside a chunk
-    const int per_row = K / 8;   // 16-byte pieces
-    const int ipr = (per_row + 63) / 64;
-    const i32x4_t xd = make_desc(reinterpret_cast<uint64_t>(L.x), (uint32_t)(M * K) * 2u);
-    const uint32_t xs = lds_addr(lds);
-    for (int t = wave; t < M * ipr; t += kWaves) {   // wave-uniform
-      const int m = t / ipr, q = t - m * ipr;
-      const int c = q * 64 + lane;
-      if (c < per_row) asm_load_lds(xd, uniform32(xs + (uint32_t)(m * xstride + q * 1024)), (uint32_t)(m * K + c * 8) * 2u);
+  // One output of a tile per thread: weight row 16 (o / 256) + o % 16, token
+  // 4 ((o / 16) % 4) + (o / 64) % 4 for thread o < 256 WR.
+  static_assert(WR * 256 <= kThreads, "an output per thread");
+  const int ln = threadIdx.x & 63, ov = (threadIdx.x >> 6) & 3, ot = threadIdx.x >> 8;
+  const int om = 4 * (ln >> 4) + ov;
+  auto out_row = [&](int tile) { return ((int64_t)tile * WR + ot) * 16 + (ln & 15); };
+  // a finished tile: the WK partial sums of every row tile, added in wave
+  // order.  red: LDS that no wave reads or writes from the barrier before on.
+  auto finish = [&](int tile, uint8_t* at, float bias) {
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(at);   // [wave][stream][lane]
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      red[(wave * NS + s) * 64 + lane] = tot[s];
+      tot[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    if constexpr (!WHOLE) {
-      const int pad = (chunks * kChunk - K) / 8;
-      for (int t = threadIdx.x; t < M * pad; t += kThreads) {
-        const int m = t / pad;
-        *reinterpret_cast<u32x4_t*>(lds + m * xstride + 2 * K + 16 * (t - m * pad)) = zero4();
+    lds_barrier();
+    const int64_t n = out_row(tile);
+    if (threadIdx.x < WR * 256 && om < M && n < L.N) {
+      float z[NS];
+#pragma unroll
+      for (int e = 0; e < NS; ++e) {
+        z[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+          const float* p = reinterpret_cast<const float*>(red + ((ot * WK + w) * NS + e) * 64 + ln);
+          z[e] += M8 ? p[ov] + p[ov + 32 * 4] : p[ov];   // up to 8 tokens: rows m and m + 8
+        }
       }
+      const float out = DUAL ? apply_act(z[0], L.act) * z[NS - 1] : apply_act(z[0] + bias, L.act);
+      const __bf16 ob = (__bf16)out;
+      L.y[(int64_t)om * L.N + n] = __builtin_bit_cast(uint16_t, ob);
     }
-    wait_vm<0>();
-    __syncthreads();
-  }
-  int i = 0;
-  for (; i + 2 < mine; i += 2) {
-    issue(C, i + 1);
-    hold(A);
-    consume(A, i);
-    issue(A, i + 2);
-    hold(C);
-    consume(C, i + 1);
-  }
-  if (i + 1 < mine) {
-    issue(C, i + 1);
-    hold(A);
-    consume(A, i);
-    hold(C);
-    consume(C, i + 1);
-  } else if (i < mine) {
-    hold(A);
-    consume(A, i);
-  }
+    lds_barrier();
+  };
 
-  // the waves' partial sums, added in wave order
-  if constexpr (XL) __syncthreads();   // every wave has read its activations
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);   // [wave][stream][lane]
-#pragma unroll
-  for (int s = 0; s < NS; ++s) red[(wave * NS + s) * 64 + lane] = tot[s];
-  __syncthreads();
-  for (int o = threadIdx.x; o < RT * 256; o += kThreads) {
-    const int ln = o & 63, v = (o >> 6) & 3, t = o >> 8;
-    const int m = 4 * (ln >> 4) + v, row = 16 * t + (ln & 15);
-    if (m >= M || row >= rows) continue;
-    float z[SETS];
-#pragma unroll
-    for (int e = 0; e < SETS; ++e) {
-      z[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) z[e] += reinterpret_cast<const float*>(red + (w * NS + t * SETS + e) * 64 + ln)[v];
+  const __amdgpu_buffer_rsrc_t dbias = w4_desc(L.bias ? L.bias : L.x, L.bias ? (uint32_t)L.N * 2u : 0u);
+  B A, C;
+  int ct = blockIdx.x, cs = 0;   // tile and step being consumed
+  // step i: the next step's activations and weights go out, then this step is
+  // multiplied.  The wait leaves the next weights in flight: loads return in
+  // order, so with no more than those outstanding the activations have landed.
+  auto step = [&](int i, B& now, B& next) {
+    if constexpr (!XL) {
+      if (i + 1 < total) stage_x(xlds + (uint32_t)(((i + 1) & 1) * xbuf), cs + 1 == steps ? 0 : cs + 1);
     }
-    float out;
-    if constexpr (DUAL) {
-      out = apply_act(z[0], L.act) * z[SETS - 1];
-    } else {
-      out = z[0];
-      if (L.bias) out += bf16_to_f32(L.bias[n0 + row]);
-      out = apply_act(out, L.act);
+    // the bias is requested ahead of the next weights: waiting for it does not
+    // wait for them.  A load in every step, with nothing to read (an offset out
+    // of range, or no bias) in all but a tile's last: behind a branch it would
+    // be waited for at once.
+    uint32_t bias = 0;
+    if constexpr (!DUAL)
+      bias = __builtin_amdgcn_raw_buffer_load_b16(dbias, cs + 1 == steps ? (int)((uint32_t)out_row(ct) * 2u) : (int)kOutOfRange, 0, 0);
+    issue(next);   // past the last step: descriptors of no rows, nothing is read
+    hold(now);
+    consume(now, cs, i & 1);
+    if constexpr (!XL) {
+      wait_vm<kLoads < 63 ? kLoads : 63>();
+      lds_barrier();
     }
-    const __bf16 ob = (__bf16)out;
-    L.y[(int64_t)m * L.N + n0 + row] = __builtin_bit_cast(uint16_t, ob);
+    if (++cs == steps) {
+      finish(ct, lds + (XL ? xbuf : (i & 1) * xbuf), __uint_as_float(bias << 16));
+      cs = 0;
+      ct += gridDim.x;
+    }
+  };
+  if constexpr (XL) {
+    // 16 lanes a unit (chunk u / M, token u % M), 4 units in flight per lane;
+    // the first are requested ahead of the weights
+    constexpr int kFly = 4, kUnits = kThreads / 16;
+    const int i16 = threadIdx.x & 15;
+    u32x4_t xv[kFly];
+    auto fetch = [&](int u0) {
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        const int u = u0 + f * kUnits, c = u / M, k = c * kChunk + i16 * 8;
+        xv[f] = u < M * chunks && k < K ? ld16(L.x + (int64_t)(u - c * M) * K + k) : zero4();
+      }
+    };
+    auto put = [&](int u0) {
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        const int u = u0 + f * kUnits, c = u / M;
+        if (u < M * chunks) put_record<GS, ZEROS>(lds + c * R.bytes, R, xv[f], u - c * M, M, i16);
+      }
+    };
+    int u = threadIdx.x >> 4;
+    fetch(u);
+    issue(A);
+    put(u);
+    for (u += kFly * kUnits; u < M * chunks; u += kFly * kUnits) {
+      fetch(u);
+      put(u);
+    }
+  } else {
+    stage_x(xlds, 0);
+    issue(A);
+    wait_vm<kLoads < 63 ? kLoads : 63>();
   }
+  lds_barrier();
+  int i = 0;
+  for (; i + 1 < total; i += 2) {
+    step(i, A, C);
+    step(i + 1, C, A);
+  }
+  if (i < total) step(i, A, C);
+  wait_vm<0>();
 }
 
-constexpr int kXMax = 64 * 1024;   // staged activations of a block
+constexpr int64_t kLdsMax = 80 * 1024;   // of a block: two blocks a CU
 
-template <bool DUAL, int GS, bool ZEROS>
-hipError_t launch_w4(const W4Layer& L, int M, hipStream_t s) {
-  constexpr int SETS = DUAL ? 2 : 1;
-  const int64_t chunks = (L.K + kChunk - 1) / kChunk;
-  const int64_t xbytes = (int64_t)M * (2 * chunks * kChunk + 16);
-  auto go = [&](auto kernel, int rt, int64_t xb) {
-    const int64_t red = (int64_t)kWaves * rt * SETS * 64 * 16;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((L.N + 16 * rt - 1) / (16 * rt))), dim3(kThreads),
-                       (unsigned)std::max(xb, red), s, L, M);
+int64_t round_up_kb(int64_t b) { return (b + 1023) / 1024 * 1024; }
+int64_t red_bytes(bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
+int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
+int64_t all_records(int64_t M, int64_t K, int G) {
+  return (K + kChunk - 1) / kChunk * (int64_t)record_of((int)M, log2_group(G)).bytes;
+}
+// the records of a call fit in LDS beside the partial sums
+bool records_in_lds(int64_t M, int64_t K, int G, bool dual) { return all_records(M, K, G) + red_bytes(dual) <= kLdsMax; }
+
+template <bool DUAL, int GS, bool ZEROS, bool M8>
+hipError_t launch_w4(const W4Layer& L, int M, int cus, hipStream_t s) {
+  const Record R = record_of(M, GS);
+  const int chunks = (int)((L.K + kChunk - 1) / kChunk);
+  auto go = [&](auto kernel, int wr, int64_t lds) {
+    const int64_t tiles = (L.N + 16 * wr - 1) / (16 * wr);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(tiles, 2 * (int64_t)cus)), dim3(kThreads), (unsigned)lds, s,
+                       L, M);
     return hipGetLastError();
   };
-  constexpr int UL = DUAL && GS < 7 ? 2 : 4;
-  if (xbytes <= kXMax) {
-    if (L.K % (UL * kChunk) == 0) return go(decode_w4_kernel<DUAL, 1, UL, GS, ZEROS, true, true>, 1, xbytes);
-    return go(decode_w4_kernel<DUAL, 1, UL, GS, ZEROS, false, true>, 1, xbytes);
+  constexpr int U = DUAL && GS < 7 ? 2 : 4;
+  if (records_in_lds(M, L.K, L.G, DUAL)) {
+    const int64_t lds = (int64_t)chunks * R.bytes + red_bytes(DUAL);
+    if (L.K % (U * kChunk) == 0) return go(decode_w4_kernel<DUAL, 1, U, GS, ZEROS, true, true, M8>, 1, lds);
+    return go(decode_w4_kernel<DUAL, 1, 2, GS, ZEROS, false, true, M8>, 1, lds);
   }
-  if (L.K % (2 * kChunk) == 0) return go(decode_w4_kernel<DUAL, 2, 2, GS, ZEROS, true, false>, 2, 0);
-  return go(decode_w4_kernel<DUAL, 2, 2, GS, ZEROS, false, false>, 2, 0);
+  if (L.records == nullptr) return hipErrorInvalidValue;
+  const int units = M * chunks;
+  hipLaunchKernelGGL((w4_records_kernel<GS, ZEROS>), dim3((unsigned)((units + kPutThreads / 16 - 1) / (kPutThreads / 16))),
+                     dim3(kPutThreads), 0, s, L.x, M, (int)L.K, chunks, L.records);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  constexpr int WR = 2, US = 2;
+  const int64_t lds = 2 * std::max<int64_t>(round_up_kb((int64_t)(kWaves / WR) * US * R.bytes), red_bytes(DUAL));
+  if (L.K % (US * kChunk) == 0) return go(decode_w4_kernel<DUAL, WR, US, GS, ZEROS, true, false, M8>, WR, lds);
+  return go(decode_w4_kernel<DUAL, WR, US, GS, ZEROS, false, false, M8>, WR, lds);
 }
 
 template <bool DUAL, int GS>
-hipError_t by_zeros(const W4Layer& L, int M, hipStream_t s) {
-  return L.z0 ? launch_w4<DUAL, GS, true>(L, M, s) : launch_w4<DUAL, GS, false>(L, M, s);
+hipError_t by_zeros(const W4Layer& L, int M, int cus, hipStream_t s) {
+  if (M <= 8) return L.z0 ? launch_w4<DUAL, GS, true, true>(L, M, cus, s) : launch_w4<DUAL, GS, false, true>(L, M, cus, s);
+  return L.z0 ? launch_w4<DUAL, GS, true, false>(L, M, cus, s) : launch_w4<DUAL, GS, false, false>(L, M, cus, s);
 }
 template <bool DUAL>
-hipError_t by_group(const W4Layer& L, int M, hipStream_t s) {
+hipError_t by_group(const W4Layer& L, int M, int cus, hipStream_t s) {
   switch (L.G) {
-    case 32: return by_zeros<DUAL, 5>(L, M, s);
-    case 64: return by_zeros<DUAL, 6>(L, M, s);
-    case 128: return by_zeros<DUAL, 7>(L, M, s);
+    case 32: return by_zeros<DUAL, 5>(L, M, cus, s);
+    case 64: return by_zeros<DUAL, 6>(L, M, cus, s);
+    case 128: return by_zeros<DUAL, 7>(L, M, cus, s);
     default: return hipErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-hipError_t launch_decode_w4(const W4Layer& L, int M, hipStream_t s) {
-  if (M < 1 || M > 16 || L.K < 32 || L.K % L.G != 0 || L.N < 1) return hipErrorInvalidValue;
+size_t decode_w4_records_bytes(int64_t M, int64_t K, int G, bool dual) {
+  return records_in_lds(M, K, G, dual) ? 0 : (size_t)all_records(M, K, G);
+}
+
+hipError_t launch_decode_w4(const W4Layer& L, int M, int cus, hipStream_t s) {
+  if (cus < 1 || M < 1 || M > 16 || L.K < 32 || L.K % L.G != 0 || L.N < 1) return hipErrorInvalidValue;
   if (L.q1 != nullptr && (L.z0 == nullptr) != (L.z1 == nullptr)) return hipErrorInvalidValue;
-  return L.q1 ? by_group<true>(L, M, s) : by_group<false>(L, M, s);
+  return L.q1 ? by_group<true>(L, M, cus, s) : by_group<false>(L, M, cus, s);
 }
 
 }  // namespace fmlp

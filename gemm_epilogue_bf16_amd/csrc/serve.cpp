@@ -21,13 +21,28 @@ fmlp_status check_w4_inner(const char* name, int64_t v, int group) {
   return FMLP_OK;
 }
 
+// sizes that a workspace is computed for (1 <= M <= 16)
+bool w4_sizes_ok(int64_t M, int64_t K, int group) {
+  return M > 0 && M <= kDecodeMaxM && K > 0 && K < kMaxInner && (group == 32 || group == 64 || group == 128);
+}
+
+uint8_t* records_at(void* workspace, size_t off) {
+  return workspace == nullptr ? nullptr : static_cast<uint8_t*>(workspace) + off;
+}
+
 }  // namespace
 
 extern "C" {
 
+size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int group) {
+  if (!w4_sizes_ok(M, K, group)) return 0;
+  const size_t records = decode_w4_records_bytes(M, K, group, false);
+  return records ? kHeader + records : 0;
+}
+
 fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf16* scales, const fmlp_bf16* zeros,
                            const fmlp_bf16* b, int act, int64_t M, int64_t K, int64_t N, int group, fmlp_bf16* y,
-                           fmlp_stream stream) {
+                           void* workspace, size_t workspace_bytes, fmlp_stream stream) {
   TRY(check_w4(M, group));
   TRY(check_w4_inner("K", K, group));
   TRY(check_inner("N", N));
@@ -38,13 +53,19 @@ fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf1
   OPTIONAL_PTR(zeros);
   OPTIONAL_PTR(b);
   TOKEN_PTR(y, M);
+  TRY(check_workspace(workspace, workspace_bytes, fmlp_linear_w4_workspace_size(M, K, group)));
   if (M == 0) return ok();
-  TRY(check_device());
-  const W4Layer L{x, Wq, scales, zeros, nullptr, nullptr, nullptr, b, y, K, N, group, act};
-  return launched(launch_decode_w4(L, (int)M, static_cast<hipStream_t>(stream)), "linear (4-bit weights) launch");
+  int cus = 0;
+  TRY(check_device(&cus));
+  const W4Layer L{x, Wq, scales, zeros, nullptr, nullptr, nullptr, b, y, K, N, group, act, records_at(workspace, kHeader)};
+  return launched(launch_decode_w4(L, (int)M, cus, static_cast<hipStream_t>(stream)), "linear (4-bit weights) launch");
 }
 
-size_t fmlp_w4_workspace_size(int64_t M, int64_t H) { return M <= 0 || H <= 0 ? 0 : kHeader + ws_bf16(M, H); }
+size_t fmlp_glu_w4_workspace_size(int64_t M, int64_t D, int64_t H, int group) {
+  if (!w4_sizes_ok(M, D, group) || !w4_sizes_ok(M, H, group)) return 0;
+  return kHeader + ws_bf16(M, H) +
+         std::max(decode_w4_records_bytes(M, D, group, true), decode_w4_records_bytes(M, H, group, false));
+}
 
 fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16* sg, const fmlp_bf16* zg,
                         const uint8_t* Wuq, const fmlp_bf16* su, const fmlp_bf16* zu, const uint8_t* Wdq,
@@ -66,15 +87,17 @@ fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16*
   OPTIONAL_PTR(zd);
   if ((zg == nullptr) != (zu == nullptr)) return fail(FMLP_E_ARG, "zg and zu must both be given or both be NULL");
   TOKEN_PTR(y, M);
-  TRY(check_workspace(workspace, workspace_bytes, fmlp_w4_workspace_size(M, H)));
+  TRY(check_workspace(workspace, workspace_bytes, fmlp_glu_w4_workspace_size(M, D, H, group)));
   if (M == 0) return ok();
-  TRY(check_device());
+  int cus = 0;
+  TRY(check_device(&cus));
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint16_t* m = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kHeader);
-  const W4Layer L1{x, Wgq, sg, zg, Wuq, su, zu, nullptr, m, D, H, group, gate_act};
-  const W4Layer L2{m, Wdq, sd, zd, nullptr, nullptr, nullptr, nullptr, y, H, D, group, FMLP_ACT_NONE};
-  HIP_TRY(launch_decode_w4(L1, (int)M, s), "glu (4-bit weights) gate+up launch");
-  return launched(launch_decode_w4(L2, (int)M, s), "glu (4-bit weights) down launch");
+  uint8_t* records = records_at(workspace, kHeader + ws_bf16(M, H));   // of x, then of m
+  const W4Layer L1{x, Wgq, sg, zg, Wuq, su, zu, nullptr, m, D, H, group, gate_act, records};
+  const W4Layer L2{m, Wdq, sd, zd, nullptr, nullptr, nullptr, nullptr, y, H, D, group, FMLP_ACT_NONE, records};
+  HIP_TRY(launch_decode_w4(L1, (int)M, cus, s), "glu (4-bit weights) gate+up launch");
+  return launched(launch_decode_w4(L2, (int)M, cus, s), "glu (4-bit weights) down launch");
 }
 
 }  // extern "C"

@@ -384,26 +384,32 @@ size_t fmlp_w8_workspace_size(int64_t M, int64_t H);
  *   scales [N, K/group] bf16, zeros [N, K/group] bf16 or NULL (then 8);
  *   W[n, k] = scales[n, k/group] * (code - zeros[n, k/group]),
  * group = 32, 64 or 128.  The calls compute what fmlp_linear and fmlp_glu
- * compute on that W: within a group x . (code - zero) is accumulated in fp32
- * from exact operands, the group's sum is multiplied by its scale in fp32, then
- * bias and activation; one rounding to bf16 (m of the gated block once more).
+ * compute on that W.  Codes are exact operands.  An activation is used as the
+ * sum of two E4M3 values of 128 k's common power of two: exact within 14
+ * binades of the largest of those 128, off by at most 2^-21 of it below.  The
+ * matrix instruction sums in fp32 and aligns neighbouring products to 13 bits
+ * before (2^-13 of a product; the output's rounding is 2^-9).  A group's sum is
+ * multiplied by its scale in fp32, then bias and activation; one rounding to
+ * bf16 (m of the gated block once more).
  * Besides the shared rules: M <= 16 (FMLP_E_ARG beyond; M == 0 is a no-op), every
  * dimension a layer contracts over (K, D, H) is a multiple of group
  * (FMLP_E_ALIGN), scales and zeros are finite, and a gated block has zero points
  * for both or neither of its gate and up weights (FMLP_E_ARG).  A token that
  * holds an infinity or a NaN gets outputs that are not finite; other tokens do
- * not see it.  One launch per layer; deterministic.  fmlp_glu_w4's workspace
- * holds m after the 8192-byte header that it leaves alone, and needs no
- * initialisation.
+ * not see it.  One launch per layer, and a small one before it where M and the
+ * layer's contraction are too large for LDS; deterministic.  The workspaces
+ * (fmlp_linear_w4: NULL where its size is 0) need no initialisation and leave
+ * the first 8192 bytes alone.
  */
 fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf16* scales, const fmlp_bf16* zeros,
                            const fmlp_bf16* b, int act, int64_t M, int64_t K, int64_t N, int group, fmlp_bf16* y,
-                           fmlp_stream stream);
+                           void* workspace, size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int group);
 fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16* sg, const fmlp_bf16* zg,
                         const uint8_t* Wuq, const fmlp_bf16* su, const fmlp_bf16* zu, const uint8_t* Wdq,
                         const fmlp_bf16* sd, const fmlp_bf16* zd, int gate_act, int64_t M, int64_t D, int64_t H,
                         int group, fmlp_bf16* y, void* workspace, size_t workspace_bytes, fmlp_stream stream);
-size_t fmlp_w4_workspace_size(int64_t M, int64_t H);
+size_t fmlp_glu_w4_workspace_size(int64_t M, int64_t D, int64_t H, int group);
 
 /*
  * y[t,:] = sum_{j<top_k} gate_w[t,j] * geglu_{expert_ids[t,j]}(x[t,:])

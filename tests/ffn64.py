@@ -165,18 +165,27 @@ def check(name, got, want, bound):
 
 
 def w4_dense(q, s, z):
-    """W and the magnitudes |s| (code + |z|) that its sums run over"""
+    """W, and |s| code and |s| |z|, which its two sums run over"""
     c = torch.stack((q & 15, q >> 4), -1).reshape(q.shape[0], -1).double()
     per = c.shape[1] // s.shape[1]
     z = torch.full_like(s, 8.0).double() if z is None else z.double()
     z, s = z.repeat_interleave(per, 1), s.double().repeat_interleave(per, 1)
-    return s * (c - z), s.abs() * (c + z.abs())
+    return s * (c - z), s.abs() * c, s.abs() * z.abs()
 
 
 def w4_linear(x, ex, q, s, z):
-    """x W^T and its error: fp32 sums of x code and of -x z, and one scale each"""
-    W, mag = w4_dense(q, s, z)
-    e = 2 * (x.shape[1] + 16) * F32 * (x.abs() @ mag.t())
+    """x W^T for x known to ex (or None), and its error:
+      * x as two E4M3 values under the power of two 2^e that brings the largest of its 128 k into (224, 448]: hi leaves at
+        most 16 of the scaled 448, lo holds that to half of 2^-9 in units of 2^(e-4), so x is kept to 2^-10 2^(e-4) <=
+        2^-14 / 224 of the largest, below 2^-21, and exactly where its last bit (2^-7 of its binade) is at least 2^-9
+        of that unit: down to 2^-13 of the largest;
+      * products of x and codes, aligned to 13 bits below a neighbour: 2^-13 each, twice that for two steps;
+      * fp32 sums of x code and of -x z, and one scale each."""
+    W, code, zero = w4_dense(q, s, z)
+    K = x.shape[1]
+    top = torch.nn.functional.pad(x.abs(), (0, -K % 128)).view(x.shape[0], -1, 128).amax(-1).repeat_interleave(128, 1)[:, :K]
+    kept = torch.where(x.abs() >= 2.0 ** -13 * top, torch.zeros_like(x), 2.0 ** -21 * top)
+    e = 2.0 ** -12 * (x.abs() @ code.t()) + kept @ code.t() + 2 * (K + 16) * F32 * (x.abs() @ (code + zero).t())
     return x @ W.t(), e if ex is None else e + ex @ W.abs().t()
 
 

@@ -118,8 +118,8 @@ def test_ckpt_sizes_and_no_tokens(L):
     assert L.fmlp_glu_ckpt_bwd_workspace_size(4096, 4096, 14336) < L.fmlp_glu_bwd_workspace_size(4096, 4096, 14336)
 
 
-def w4(L, x=X, q=Q, s=S, z=B, b=B, act=4, M=4, K=256, N=72, g=64, y=Y):
-    return L.fmlp_linear_w4(x, q, s, z, b, act, M, K, N, g, y, None)
+def w4(L, x=X, q=Q, s=S, z=B, b=B, act=4, M=4, K=256, N=72, g=64, y=Y, ws=None, nb=0):
+    return L.fmlp_linear_w4(x, q, s, z, b, act, M, K, N, g, y, ws, nb, None)
 
 
 def glu_w4(L, x=X, q=Q, s=S, zg=B, zu=B, zd=B, act=4, M=4, D=256, H=128, g=64, y=Y, ws=WS, nb=BIG):
@@ -136,7 +136,9 @@ FOUR = [
 
 @pytest.mark.parametrize("kw,status,msg", FOUR + [
     (dict(K=288), E_ALIGN, "K=288"), (dict(K=0), E_SHAPE, "K=0"), (dict(N=20), E_ALIGN, "N=20"), (dict(N=1 << 22), E_SHAPE, "N="),
-    (dict(z=B + 8), E_ALIGN, "zeros is not"), (dict(b=B + 8), E_ALIGN, "b is not")])
+    (dict(z=B + 8), E_ALIGN, "zeros is not"), (dict(b=B + 8), E_ALIGN, "b is not"),
+    (dict(M=16, K=4096), E_WS, "NULL"), (dict(M=16, K=4096, ws=WS, nb=8192), E_WS, "needs"),
+    (dict(M=16, K=4096, ws=WS + 8, nb=BIG), E_ALIGN, "workspace")])
 def test_linear_w4_validation(L, kw, status, msg):
     assert w4(L, **kw) == status and msg in _err(L)
 
@@ -149,7 +151,14 @@ def test_glu_w4_validation(L, kw, status, msg):
 
 
 def test_w4_sizes_and_no_tokens(L):
-    assert L.fmlp_w4_workspace_size(4, 128) == 8192 + 1024 and L.fmlp_w4_workspace_size(0, 128) == 0
+    # activations that fit in LDS need no scratch; 16 tokens: 32 slots of 128, 32 exponents and 16 sums a group, per chunk
+    assert L.fmlp_linear_w4_workspace_size(4, 4096, 64) == 0
+    assert L.fmlp_linear_w4_workspace_size(16, 4096, 64) == 8192 + 32 * (4096 + 32 + 2 * 64)
+    assert L.fmlp_linear_w4_workspace_size(16, 4128, 32) == 8192 + 33 * (4096 + 32 + 4 * 64)
+    assert L.fmlp_linear_w4_workspace_size(0, 4096, 64) == 0 and L.fmlp_linear_w4_workspace_size(4, 4096, 48) == 0
+    assert L.fmlp_glu_w4_workspace_size(4, 256, 128, 64) == 8192 + 1024
+    assert L.fmlp_glu_w4_workspace_size(0, 256, 128, 64) == 0 and L.fmlp_glu_w4_workspace_size(17, 256, 128, 64) == 0
+    assert L.fmlp_glu_w4_workspace_size(16, 4096, 14336, 64) == 8192 + 16 * 14336 * 2 + 112 * (4096 + 32 + 2 * 64)
     assert w4(L, M=0, x=None, y=None) == OK
     assert glu_w4(L, M=0, x=None, y=None, ws=None, nb=0) == OK
     assert w4(L, M=0, x=None, y=None, q=None) == E_NULL
