@@ -175,7 +175,7 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = _sz
         L.fmlp_linear_w4.argtypes = [_p, _p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _sz, _p]
         L.fmlp_glu_w4.argtypes = [_p] * 10 + [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _sz, _p]
-        L.fmlp_linear_w4_workspace_size.argtypes = [_i64, _i64, ctypes.c_int]
+        L.fmlp_linear_w4_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int]
         L.fmlp_linear_w4_workspace_size.restype = _sz
         L.fmlp_glu_w4_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int]
         L.fmlp_glu_w4_workspace_size.restype = _sz
@@ -944,7 +944,7 @@ def _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace):
     y = _out("out", out, x.shape[:-1] + (N,), x)
     L = lib()
     M = x.numel() // K
-    need = L.fmlp_linear_w4_workspace_size(M, K, G)
+    need = L.fmlp_linear_w4_workspace_size(M, K, N, G)
     ws = _scratch(x, workspace, need) if need else None
     return BoundCall(L.fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act],
                                         M, K, N, G, y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),

@@ -12,7 +12,7 @@ namespace fmlp {
 // G = 32, 64 or 128 and K % G == 0.  With q1 set it is the gate+up layer
 // y = act(x W0^T) * (x W1^T) (z0 and z1 both null or both set), else
 // y = act(x W0^T + bias).  One launch,
-// or two where the activations need records.
+// up to three where the activations are large.
 struct W4Layer {
   const uint16_t* x;     // [M, K] bf16
   const uint8_t* q0;     // [N, K / 2], code 2j in the low half of byte j
@@ -26,13 +26,13 @@ struct W4Layer {
   int64_t K, N;
   int G;
   int act;               // Act; for a gated layer, the gate's activation
-  uint8_t* records;      // decode_w4_records_bytes of device scratch, or nullptr where that is 0
+  uint8_t* scratch;      // decode_w4_scratch_bytes of device memory, or nullptr where that is 0
+  uint8_t* records;      // (set by the launcher)
 };
 
-// Scratch for activations that do not fit in LDS (0 where they do); one more,
-// small, launch writes it.
-size_t decode_w4_records_bytes(int64_t M, int64_t K, int G, bool dual);
-
+// Scratch of a call: activations in operand form where a block does not make
+// them itself, and the k slices' sums where they do not all fit in LDS.
+size_t decode_w4_scratch_bytes(int64_t M, int64_t K, int64_t N, int G, bool dual);
 // cus: the device's compute units (the persistent grid's size).
 hipError_t launch_decode_w4(const W4Layer& L, int M, int cus, hipStream_t s);
 

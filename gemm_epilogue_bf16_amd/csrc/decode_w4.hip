@@ -43,16 +43,18 @@
 // A block's 8 waves are WR row tiles (16 rows each, gate and up rows for a
 // gated layer) times WK parts of k.  The grid is persistent (two blocks a CU)
 // and a block's work is one stream of steps (U chunks per wave) through its
-// tiles, double-buffered in registers: the next tile's first weights are in
-// flight while a tile is finished.  Partial sums of the WK waves meet in LDS
+// tiles, with two steps' weights in flight in registers, across tiles.  Partial sums of the WK waves meet in LDS
 // in wave order (deterministic).
 //
-// Activations in LDS are records, one per chunk: hi and lo of every token in
-// operand order, their exponents, and the groups' sums.  Up to 64 KB of them a
-// block makes its own from x once, while its first weights are in flight.
-// Larger sets are made once per call by a small kernel into the workspace and
-// stream through LDS with the weights, a step at a time (1 KB pieces by loads
-// that write LDS, two buffers, one barrier a step).
+// Activations live in LDS as records, one per chunk: hi and lo of every token in
+// operand order, their exponents, and the groups' sums.  Up to 256 of them
+// (tokens x chunks) a block makes its own from x, while its first weights are
+// in flight; more are made once per call by a small kernel into the workspace
+// and copied to LDS.  Where all records do not fit, k is cut into slices that
+// do: each slice has its share of the blocks, the slices' sums go to the
+// workspace in fp32 and a last small kernel adds them in order.  (Streaming the
+// records through LDS beside the weights, a step at a time, made every step
+// wait for its records: 60 us against %%% for 16 tokens through 8192 -> 28672.)
 #include <algorithm>
 
 #include "common.h"
@@ -63,19 +65,21 @@ namespace fmlp {
 
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 16;   // one block a CU
 constexpr int kThreads = kWaves * 64;
 constexpr int kChunk = 128;   // k of one 16-byte load of the 4 lanes of a row
 
+// A raw buffer of `bytes` at base, both wave-uniform: readfirstlane says so to
+// the compiler, which computes tile addresses on the vector unit and would
+// issue every load in a loop over the lanes' descriptors (and drain all loads
+// before it).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t w4_desc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)uniform32((uint32_t)(a >> 32)) << 32 | uniform32((uint32_t)a);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), (short)0, (int)uniform32(bytes), 0x00020000);
 }
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t d, uint32_t off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(d, (int)off, 0, 0));
-}
-// weights are read exactly once: non-temporal
-__device__ __forceinline__ u32x4_t load16_stream(__amdgpu_buffer_rsrc_t d, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(d, (int)off, 0, 2));
 }
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
@@ -98,6 +102,12 @@ __host__ __device__ __forceinline__ Record record_of(int M, int gs) {
   return r;
 }
 
+// v of another lane of the row of 16 (the DPP control says which)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+
 // 16 lanes (i = 0 .. 15) put one token's chunk into its record: lane i has k
 // 8 i .. 8 i + 7 (zeros past K).
 template <int GS, bool ZEROS>
@@ -111,10 +121,14 @@ __device__ __forceinline__ void put_record(uint8_t* rec, const Record& R, const 
     top = fmaxf(top, a < __builtin_inff() ? a : 0.f);
     sum += v[j];
   }
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-#pragma unroll
-  for (int d = 1; d < (1 << GS) / 8; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  top = fmaxf(top, dpp<0xB1>(top));    // quad_perm 1 0 3 2
+  top = fmaxf(top, dpp<0x4E>(top));    // quad_perm 2 3 0 1
+  top = fmaxf(top, dpp<0x141>(top));   // row_half_mirror: the other quad of 8
+  top = fmaxf(top, dpp<0x140>(top));   // row_mirror: the other 8 of 16
+  sum += dpp<0xB1>(sum);
+  sum += dpp<0x4E>(sum);
+  if constexpr (GS > 5) sum += dpp<0x141>(sum);
+  if constexpr (GS > 6) sum += dpp<0x140>(sum);
   const uint32_t bits = __float_as_uint(top);
   // at least -122: the lo part's exponent byte stays positive
   const int e = max((int)(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), -122);
@@ -231,73 +245,83 @@ struct Values {
   }
 };
 
-// NS weight streams (gate and up), U chunks each
+// A wave's step: NS weight streams (gate and up) of U chunks, and the bias of the
+// tile's 16 rows with its last step (nothing is read in the others).
 template <int NS, int U, int NV, bool WHOLE, bool ZEROS>
 struct Batch {
   u32x4_t w[NS][U];
   Values<NV, WHOLE> s[NS];
   Values<ZEROS ? NV : 2, WHOLE> z[ZEROS ? NS : 1];
+  uint32_t bias;
 };
 
-// GS: log2 of the group size.  WHOLE: K is a multiple of U chunks, so a step
-// exists in full or not at all and scales come as aligned vectors.  XL: all
-// records in LDS, made here.  M8: at most 8 tokens.
-template <bool DUAL, int WR, int U, int GS, bool ZEROS, bool WHOLE, bool XL, bool M8>
-__global__ __launch_bounds__(kThreads, 4) void decode_w4_kernel(W4Layer L, int M) {
+// How a call is cut: k slices of `chunks` chunks each (the last may have fewer),
+// with per_slice blocks each; parts: [slice][set][M][N] fp32, or nullptr (one slice).
+struct W4Cut {
+  int slices, chunks, per_slice;
+  float* parts;
+};
+
+// GS: log2 of the group size.  WHOLE: a slice is a multiple of U chunks, so a
+// step exists in full or not at all and scales come as aligned vectors.  M8: at
+// most 8 tokens.
+template <bool DUAL, int U, int GS, bool ZEROS, bool WHOLE, bool M8>
+__global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W4Cut cut) {
   constexpr int NS = DUAL ? 2 : 1;
-  constexpr int WK = kWaves / WR;
   constexpr int GPC = kChunk >> GS;        // groups per chunk
   constexpr int NV = U * GPC;              // scales of a step
-  constexpr int SC = WK * U;               // chunks of a block's step
+  constexpr int SC = kWaves * U;           // chunks of a block's step
   using B = Batch<NS, U, NV, WHOLE, ZEROS>;
   // load instructions of a step's weights, scales and zero points
-  constexpr int kLoads = NS * (U + (ZEROS ? 2 : 1) * Values<NV, WHOLE>::kLoads);
+  constexpr int kLoads = NS * (U + (ZEROS ? 2 : 1) * Values<NV, WHOLE>::kLoads) + (DUAL ? 0 : 1);
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / WK, wk = wave % WK;
   const int r = lane & 15;   // weight row of a tile; row of the activation operand
   const int g = lane >> 4;
   const int K = (int)L.K;
   const int groups = K >> GS;
-  const int chunks = (K + kChunk - 1) / kChunk;
+  const int slice = blockIdx.x % cut.slices, first = blockIdx.x / cut.slices;   // the block's slice, its first tile
+  const int cb = slice * cut.chunks;                                              // first chunk of the slice
+  const int chunks = min((K + kChunk - 1) / kChunk - cb, cut.chunks);
   const int steps = (chunks + SC - 1) / SC;   // of a tile
-  const int tiles = (int)((L.N + 16 * WR - 1) / (16 * WR));
-  const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // grid <= tiles
-  const int total = mine * steps;
+  const int tiles = (int)((L.N + 15) / 16);
+  const int total = (tiles - first + cut.per_slice - 1) / cut.per_slice * steps;   // per_slice <= tiles
   const Record R = record_of(M, GS);
 
   const uint32_t wlane = (uint32_t)(r * (K / 2) + g * 16);
   const uint32_t slane = (uint32_t)(r * groups) * 2u;
   constexpr int kRed = kWaves * NS * 64 * 16;   // the partial sums of a tile
-  const int xbuf = XL ? chunks * R.bytes : max((SC * R.bytes + 1023) / 1024 * 1024, kRed);   // an activation buffer
   // the lane's slot (rows without a token read slot 0; their results are not used)
   const int slot = M8 ? ((r & 7) < M ? (r & 7) + (r >> 3) * M : 0) : (r < M ? r : 0);
   const int xop = g * (R.slots * 16) + slot * 16;    // the lane's operand bytes in a record, first half
   const int xsum = R.sums + 16 * (M8 ? (R.tokens == 8 ? g & 1 : 0) : g);   // the sums of its 4 result rows' tokens
 
-  int it = blockIdx.x, is = 0;   // tile and step of the next weights issued
+  const __amdgpu_buffer_rsrc_t dbias = w4_desc(L.bias ? L.bias : L.x, L.bias ? (uint32_t)L.N * 2u : 0u);
+  int it = first, is = 0;   // tile and step of the next weights issued
   auto issue = [&](B& b) {
-    const int64_t n0 = ((int64_t)it * WR + wr) * 16;
+    const int64_t n0 = (int64_t)it * 16;
     const int rows = (int)max<int64_t>(min<int64_t>(16, L.N - n0), 0);
-    const int c0 = (is * WK + wk) * U;
+    const int c0 = (is * kWaves + wave) * U;   // within the slice
     const bool any = c0 < chunks;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const __amdgpu_buffer_rsrc_t dw = w4_desc((s ? L.q1 : L.q0) + n0 * (K / 2), (uint32_t)rows * (uint32_t)(K / 2));
       const __amdgpu_buffer_rsrc_t ds = w4_desc((s ? L.s1 : L.s0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u);
-      const uint32_t wo = wlane + (any ? (uint32_t)c0 * 64u : kOutOfRange);
+      const uint32_t wo = wlane + (any ? (uint32_t)(cb + c0) * 64u : kOutOfRange);
 #pragma unroll
-      for (int j = 0; j < U; ++j) b.w[s][j] = load16_stream(dw, WHOLE || c0 + j < chunks ? wo + 64u * j : kOutOfRange);
-      const uint32_t so = slane + (any ? (uint32_t)(c0 * GPC) * 2u : kOutOfRange);
-      b.s[s].load(ds, so, groups - c0 * GPC);
+      for (int j = 0; j < U; ++j) b.w[s][j] = load16(dw, WHOLE || c0 + j < chunks ? wo + 64u * j : kOutOfRange);
+      const uint32_t so = slane + (any ? (uint32_t)((cb + c0) * GPC) * 2u : kOutOfRange);
+      b.s[s].load(ds, so, min(groups - cb * GPC, chunks * GPC) - c0 * GPC);
       if constexpr (ZEROS)
-        b.z[s].load(w4_desc((s ? L.z1 : L.z0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u), so, groups - c0 * GPC);
+        b.z[s].load(w4_desc((s ? L.z1 : L.z0) + n0 * groups, (uint32_t)rows * (uint32_t)groups * 2u), so, min(groups - cb * GPC, chunks * GPC) - c0 * GPC);
     }
+    if constexpr (!DUAL)
+      b.bias = __builtin_amdgcn_raw_buffer_load_b16(dbias, is + 1 == steps ? (int)((uint32_t)(it * 16 + r) * 2u) : (int)kOutOfRange, 0, 0);
     if (++is == steps) {
       is = 0;
-      it += gridDim.x;
+      it += cut.per_slice;
     }
   };
   auto hold = [&](B& b) {
@@ -308,17 +332,8 @@ __global__ __launch_bounds__(kThreads, 4) void decode_w4_kernel(W4Layer L, int M
       b.s[s].hold();
       if constexpr (ZEROS) b.z[s].hold();
     }
+    if constexpr (!DUAL) asm volatile("" : "+v"(b.bias));
   };
-  // the records of a step into the LDS buffer at `base`, 1 KB per instruction
-  const i32x4_t xd = make_desc(reinterpret_cast<uint64_t>(L.records), (uint32_t)(XL ? 0 : chunks * R.bytes));
-  auto stage_x = [&](uint32_t base, int step) {
-    const int off = step * SC * R.bytes;
-    const int pieces = (SC * R.bytes + 1023) / 1024;
-    for (int t = wave; t < pieces; t += kWaves)   // wave-uniform
-      asm_load_lds(xd, uniform32(base + (uint32_t)(t * 1024)), (uint32_t)(off + t * 1024 + lane * 16));
-  };
-  const uint32_t xlds = lds_addr(lds);
-
   f32x4_t tot[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) tot[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -341,9 +356,9 @@ __global__ __launch_bounds__(kThreads, 4) void decode_w4_kernel(W4Layer L, int M
     }
     return v;
   };
-  auto consume = [&](const B& b, int step, int buf) {
-    const int c0 = (step * WK + wk) * U;
-    const uint8_t* recs = lds + (XL ? c0 * R.bytes : buf * xbuf + wk * U * R.bytes);
+  auto consume = [&](const B& b, int step) {
+    const int c0 = (step * kWaves + wave) * U;
+    const uint8_t* recs = lds + c0 * R.bytes;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (WHOLE ? c0 >= chunks : c0 + j >= chunks) break;   // wave-uniform
@@ -382,150 +397,173 @@ __global__ __launch_bounds__(kThreads, 4) void decode_w4_kernel(W4Layer L, int M
       }
     }
   };
-  // One output of a tile per thread: weight row 16 (o / 256) + o % 16, token
-  // 4 ((o / 16) % 4) + (o / 64) % 4 for thread o < 256 WR.
-  static_assert(WR * 256 <= kThreads, "an output per thread");
-  const int ln = threadIdx.x & 63, ov = (threadIdx.x >> 6) & 3, ot = threadIdx.x >> 8;
-  const int om = 4 * (ln >> 4) + ov;
-  auto out_row = [&](int tile) { return ((int64_t)tile * WR + ot) * 16 + (ln & 15); };
-  // a finished tile: the WK partial sums of every row tile, added in wave
-  // order.  red: LDS that no wave reads or writes from the barrier before on.
-  auto finish = [&](int tile, uint8_t* at, float bias) {
-    f32x4_t* red = reinterpret_cast<f32x4_t*>(at);   // [wave][stream][lane]
+  // One output of a tile per thread o < 256: weight row o % 16, token
+  // 4 ((o / 16) % 4) + (o / 64) % 4.
+  const int ov = (threadIdx.x >> 6) & 3, om = 4 * g + ov;
+  // A finished tile: the waves' partial sums, added in wave order.  Two tiles'
+  // sums alternate in LDS, so one barrier a tile is enough: a wave writes a
+  // tile's sums after the barrier that every reader of those two tiles before
+  // has reached.
+  auto finish = [&](int tile, int parity, float bias) {
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + chunks * R.bytes + parity * kRed);   // [wave][stream][lane]
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       red[(wave * NS + s) * 64 + lane] = tot[s];
       tot[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     lds_barrier();
-    const int64_t n = out_row(tile);
-    if (threadIdx.x < WR * 256 && om < M && n < L.N) {
+    const int64_t n = (int64_t)tile * 16 + r;
+    if (threadIdx.x < 256 && om < M && n < L.N) {
       float z[NS];
 #pragma unroll
       for (int e = 0; e < NS; ++e) {
         z[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WK; ++w) {
-          const float* p = reinterpret_cast<const float*>(red + ((ot * WK + w) * NS + e) * 64 + ln);
+        for (int w = 0; w < kWaves; ++w) {
+          const float* p = reinterpret_cast<const float*>(red + (w * NS + e) * 64 + lane);
           z[e] += M8 ? p[ov] + p[ov + 32 * 4] : p[ov];   // up to 8 tokens: rows m and m + 8
         }
       }
-      const float out = DUAL ? apply_act(z[0], L.act) * z[NS - 1] : apply_act(z[0] + bias, L.act);
-      const __bf16 ob = (__bf16)out;
-      L.y[(int64_t)om * L.N + n] = __builtin_bit_cast(uint16_t, ob);
+      if (cut.parts) {
+#pragma unroll
+        for (int e = 0; e < NS; ++e) cut.parts[((int64_t)(slice * NS + e) * M + om) * L.N + n] = z[e];
+      } else {
+        const float out = DUAL ? apply_act(z[0], L.act) * z[NS - 1] : apply_act(z[0] + bias, L.act);
+        const __bf16 ob = (__bf16)out;
+        L.y[(int64_t)om * L.N + n] = __builtin_bit_cast(uint16_t, ob);
+      }
     }
-    lds_barrier();
   };
 
-  const __amdgpu_buffer_rsrc_t dbias = w4_desc(L.bias ? L.bias : L.x, L.bias ? (uint32_t)L.N * 2u : 0u);
   B A, C;
-  int ct = blockIdx.x, cs = 0;   // tile and step being consumed
-  // step i: the next step's activations and weights go out, then this step is
-  // multiplied.  The wait leaves the next weights in flight: loads return in
-  // order, so with no more than those outstanding the activations have landed.
-  auto step = [&](int i, B& now, B& next) {
-    if constexpr (!XL) {
-      if (i + 1 < total) stage_x(xlds + (uint32_t)(((i + 1) & 1) * xbuf), cs + 1 == steps ? 0 : cs + 1);
-    }
-    // the bias is requested ahead of the next weights: waiting for it does not
-    // wait for them.  A load in every step, with nothing to read (an offset out
-    // of range, or no bias) in all but a tile's last: behind a branch it would
-    // be waited for at once.
-    uint32_t bias = 0;
-    if constexpr (!DUAL)
-      bias = __builtin_amdgcn_raw_buffer_load_b16(dbias, cs + 1 == steps ? (int)((uint32_t)out_row(ct) * 2u) : (int)kOutOfRange, 0, 0);
-    issue(next);   // past the last step: descriptors of no rows, nothing is read
+  int ct = first, cs = 0, parity = 0;   // tile and step being consumed
+  // A step's weights are multiplied and their registers take those of the step
+  // after the next.
+  auto step = [&](B& now) {
     hold(now);
-    consume(now, cs, i & 1);
-    if constexpr (!XL) {
-      wait_vm<kLoads < 63 ? kLoads : 63>();
-      lds_barrier();
-    }
+    consume(now, cs);
+    const float bias = DUAL ? 0.f : __uint_as_float(now.bias << 16);
+    issue(now);   // past the last step: descriptors of no rows, nothing is read
     if (++cs == steps) {
-      finish(ct, lds + (XL ? xbuf : (i & 1) * xbuf), __uint_as_float(bias << 16));
+      finish(ct, parity, bias);
+      parity ^= 1;
       cs = 0;
-      ct += gridDim.x;
+      ct += cut.per_slice;
     }
   };
-  if constexpr (XL) {
-    // 16 lanes a unit (chunk u / M, token u % M), 4 units in flight per lane;
-    // the first are requested ahead of the weights
-    constexpr int kFly = 4, kUnits = kThreads / 16;
+  // The first step's weights go out before the records are made, the second's
+  // after: a CU takes only so many requests, and with both ahead every wave
+  // stood in its second step's issue until the first had arrived (7 us).
+  if (L.records) {   // made by the kernel before
+    const uint32_t xlds = lds_addr(lds);
+    const int bytes = chunks * R.bytes;
+    const i32x4_t rd = make_desc(reinterpret_cast<uint64_t>(L.records + (int64_t)cb * R.bytes), (uint32_t)bytes);
+    for (int t = wave; t * 1024 < bytes; t += kWaves)   // wave-uniform; the last piece's lanes past the end write nothing
+      if (t * 1024 + lane * 16 < bytes) asm_load_lds(rd, uniform32(xlds + (uint32_t)(t * 1024)), (uint32_t)(t * 1024 + lane * 16));
+    issue(A);
+    wait_vm<kLoads < 63 ? kLoads : 63>();   // loads return in order: all but the weights have landed
+  } else {
+    // 16 lanes a unit (chunk u / M, token u % M)
+    constexpr int kUnits = kThreads / 16;
     const int i16 = threadIdx.x & 15;
-    u32x4_t xv[kFly];
-    auto fetch = [&](int u0) {
-#pragma unroll
-      for (int f = 0; f < kFly; ++f) {
-        const int u = u0 + f * kUnits, c = u / M, k = c * kChunk + i16 * 8;
-        xv[f] = u < M * chunks && k < K ? ld16(L.x + (int64_t)(u - c * M) * K + k) : zero4();
-      }
-    };
-    auto put = [&](int u0) {
-#pragma unroll
-      for (int f = 0; f < kFly; ++f) {
-        const int u = u0 + f * kUnits, c = u / M;
-        if (u < M * chunks) put_record<GS, ZEROS>(lds + c * R.bytes, R, xv[f], u - c * M, M, i16);
-      }
+    auto fetch = [&](int u) {
+      const int c = u / M, k = (cb + c) * kChunk + i16 * 8;
+      return u < M * chunks && k < K ? ld16(L.x + (int64_t)(u - c * M) * K + k) : zero4();
     };
     int u = threadIdx.x >> 4;
-    fetch(u);
+    u32x4_t xv = fetch(u), xn = fetch(u + kUnits);
     issue(A);
-    put(u);
-    for (u += kFly * kUnits; u < M * chunks; u += kFly * kUnits) {
-      fetch(u);
-      put(u);
+#pragma clang loop unroll(disable)
+    for (; u < M * chunks; u += kUnits) {
+      const int c = u / M;
+      put_record<GS, ZEROS>(lds + c * R.bytes, R, xv, u - c * M, M, i16);
+      xv = xn;
+      xn = fetch(u + 2 * kUnits);
     }
-  } else {
-    stage_x(xlds, 0);
-    issue(A);
-    wait_vm<kLoads < 63 ? kLoads : 63>();
   }
   lds_barrier();
+  issue(C);
   int i = 0;
   for (; i + 1 < total; i += 2) {
-    step(i, A, C);
-    step(i + 1, C, A);
+    step(A);
+    step(C);
   }
-  if (i < total) step(i, A, C);
+  if (i < total) step(A);
   wait_vm<0>();
 }
 
-constexpr int64_t kLdsMax = 80 * 1024;   // of a block: two blocks a CU
-
-int64_t round_up_kb(int64_t b) { return (b + 1023) / 1024 * 1024; }
-int64_t red_bytes(bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
-int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
-int64_t all_records(int64_t M, int64_t K, int G) {
-  return (K + kChunk - 1) / kChunk * (int64_t)record_of((int)M, log2_group(G)).bytes;
+// y = act(sum of the slices + bias), or act(gate) * up: one thread per output.
+template <bool DUAL>
+__global__ __launch_bounds__(256) void w4_sum_kernel(W4Layer L, int M, W4Cut cut) {
+  const int64_t MN = (int64_t)M * L.N;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= MN) return;
+  float z = 0.f, u = 0.f;
+  for (int s = 0; s < cut.slices; ++s) {
+    z += cut.parts[(int64_t)s * (DUAL ? 2 : 1) * MN + i];
+    if (DUAL) u += cut.parts[((int64_t)s * 2 + 1) * MN + i];
+  }
+  if (!DUAL && L.bias) z += bf16_to_f32(L.bias[i % L.N]);
+  const __bf16 o = (__bf16)(DUAL ? apply_act(z, L.act) * u : apply_act(z, L.act));
+  L.y[i] = __builtin_bit_cast(uint16_t, o);
 }
-// the records of a call fit in LDS beside the partial sums
-bool records_in_lds(int64_t M, int64_t K, int G, bool dual) { return all_records(M, K, G) + red_bytes(dual) <= kLdsMax; }
+
+constexpr int64_t kLdsMax = 160 * 1024;   // of a block, one a CU
+constexpr int kUnitsInside = 256;         // tokens x chunks whose records a block makes itself
+
+int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
+int64_t red_bytes(bool dual) { return 2 * (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
+
+// The k slices of a call: as few as have records that fit in LDS, of equal
+// numbers of chunks (a multiple of 4, so that every slice starts on whole steps).
+W4Cut cut_of(int64_t M, int64_t K, int G, bool dual) {
+  const int64_t chunks = (K + kChunk - 1) / kChunk;
+  const int64_t fit = (kLdsMax - red_bytes(dual)) / record_of((int)M, log2_group(G)).bytes / 4 * 4;
+  W4Cut c{};
+  const int64_t slices = (chunks + fit - 1) / fit;
+  c.chunks = (int)(((chunks + slices - 1) / slices + 3) / 4 * 4);
+  c.slices = (int)((chunks + c.chunks - 1) / c.chunks);
+  return c;
+}
+bool made_inside(int64_t M, const W4Cut& c) { return M * c.chunks <= kUnitsInside; }
+size_t records_bytes(int64_t M, int64_t K, int G, const W4Cut& c) {
+  const size_t b = (size_t)((K + kChunk - 1) / kChunk) * (size_t)record_of((int)M, log2_group(G)).bytes;
+  return made_inside(M, c) ? 0 : (b + 255) / 256 * 256;
+}
 
 template <bool DUAL, int GS, bool ZEROS, bool M8>
 hipError_t launch_w4(const W4Layer& L, int M, int cus, hipStream_t s) {
-  const Record R = record_of(M, GS);
   const int chunks = (int)((L.K + kChunk - 1) / kChunk);
-  auto go = [&](auto kernel, int wr, int64_t lds) {
-    const int64_t tiles = (L.N + 16 * wr - 1) / (16 * wr);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(tiles, 2 * (int64_t)cus)), dim3(kThreads), (unsigned)lds, s,
-                       L, M);
+  W4Cut cut = cut_of(M, L.K, L.G, DUAL);
+  const size_t records = records_bytes(M, L.K, L.G, cut);
+  if ((records || cut.slices > 1) && L.scratch == nullptr) return hipErrorInvalidValue;
+  W4Layer P = L;
+  P.records = records ? L.scratch : nullptr;
+  if (records) {
+    const int units = M * chunks;
+    hipLaunchKernelGGL((w4_records_kernel<GS, ZEROS>), dim3((unsigned)((units + kPutThreads / 16 - 1) / (kPutThreads / 16))),
+                       dim3(kPutThreads), 0, s, L.x, M, (int)L.K, chunks, P.records);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  const int64_t tiles = (L.N + 15) / 16;
+  if (cut.slices > 1) cut.parts = reinterpret_cast<float*>(L.scratch + records);
+  cut.per_slice = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cus / cut.slices));
+  const int64_t lds = std::min(chunks, cut.chunks) * (int64_t)record_of(M, GS).bytes + red_bytes(DUAL);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(cut.per_slice * cut.slices)), dim3(kThreads), (unsigned)lds, s, P, M, cut);
     return hipGetLastError();
   };
-  constexpr int U = DUAL && GS < 7 ? 2 : 4;
-  if (records_in_lds(M, L.K, L.G, DUAL)) {
-    const int64_t lds = (int64_t)chunks * R.bytes + red_bytes(DUAL);
-    if (L.K % (U * kChunk) == 0) return go(decode_w4_kernel<DUAL, 1, U, GS, ZEROS, true, true, M8>, 1, lds);
-    return go(decode_w4_kernel<DUAL, 1, 2, GS, ZEROS, false, true, M8>, 1, lds);
-  }
-  if (L.records == nullptr) return hipErrorInvalidValue;
-  const int units = M * chunks;
-  hipLaunchKernelGGL((w4_records_kernel<GS, ZEROS>), dim3((unsigned)((units + kPutThreads / 16 - 1) / (kPutThreads / 16))),
-                     dim3(kPutThreads), 0, s, L.x, M, (int)L.K, chunks, L.records);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  constexpr int WR = 2, US = 2;
-  const int64_t lds = 2 * std::max<int64_t>(round_up_kb((int64_t)(kWaves / WR) * US * R.bytes), red_bytes(DUAL));
-  if (L.K % (US * kChunk) == 0) return go(decode_w4_kernel<DUAL, WR, US, GS, ZEROS, true, false, M8>, WR, lds);
-  return go(decode_w4_kernel<DUAL, WR, US, GS, ZEROS, false, false, M8>, WR, lds);
+  constexpr int U = (DUAL || (GS == 5 && ZEROS && !M8)) && GS < 7 ? 2 : 4;
+  hipError_t e;
+  if (U == 4 && cut.chunks >= kWaves * 4 && L.K % (4 * kChunk) == 0)
+    e = go(decode_w4_kernel<DUAL, U, GS, ZEROS, true, M8>);
+  else if (L.K % (2 * kChunk) == 0)
+    e = go(decode_w4_kernel<DUAL, 2, GS, ZEROS, true, M8>);
+  else
+    e = go(decode_w4_kernel<DUAL, 2, GS, ZEROS, false, M8>);
+  if (e != hipSuccess || cut.slices == 1) return e;
+  hipLaunchKernelGGL((w4_sum_kernel<DUAL>), dim3((unsigned)(((int64_t)M * L.N + 255) / 256)), dim3(256), 0, s, P, M, cut);
+  return hipGetLastError();
 }
 
 template <bool DUAL, int GS>
@@ -545,8 +583,9 @@ hipError_t by_group(const W4Layer& L, int M, int cus, hipStream_t s) {
 
 }  // namespace
 
-size_t decode_w4_records_bytes(int64_t M, int64_t K, int G, bool dual) {
-  return records_in_lds(M, K, G, dual) ? 0 : (size_t)all_records(M, K, G);
+size_t decode_w4_scratch_bytes(int64_t M, int64_t K, int64_t N, int G, bool dual) {
+  const W4Cut c = cut_of(M, K, G, dual);
+  return records_bytes(M, K, G, c) + (c.slices > 1 ? (size_t)c.slices * (dual ? 2 : 1) * (size_t)M * (size_t)N * 4 : 0);
 }
 
 hipError_t launch_decode_w4(const W4Layer& L, int M, int cus, hipStream_t s) {

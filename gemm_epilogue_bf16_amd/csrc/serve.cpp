@@ -26,7 +26,7 @@ bool w4_sizes_ok(int64_t M, int64_t K, int group) {
   return M > 0 && M <= kDecodeMaxM && K > 0 && K < kMaxInner && (group == 32 || group == 64 || group == 128);
 }
 
-uint8_t* records_at(void* workspace, size_t off) {
+uint8_t* scratch_at(void* workspace, size_t off) {
   return workspace == nullptr ? nullptr : static_cast<uint8_t*>(workspace) + off;
 }
 
@@ -34,10 +34,10 @@ uint8_t* records_at(void* workspace, size_t off) {
 
 extern "C" {
 
-size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int group) {
-  if (!w4_sizes_ok(M, K, group)) return 0;
-  const size_t records = decode_w4_records_bytes(M, K, group, false);
-  return records ? kHeader + records : 0;
+size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int64_t N, int group) {
+  if (!w4_sizes_ok(M, K, group) || N <= 0 || N >= kMaxInner) return 0;
+  const size_t scratch = decode_w4_scratch_bytes(M, K, N, group, false);
+  return scratch ? kHeader + scratch : 0;
 }
 
 fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf16* scales, const fmlp_bf16* zeros,
@@ -53,18 +53,18 @@ fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf1
   OPTIONAL_PTR(zeros);
   OPTIONAL_PTR(b);
   TOKEN_PTR(y, M);
-  TRY(check_workspace(workspace, workspace_bytes, fmlp_linear_w4_workspace_size(M, K, group)));
+  TRY(check_workspace(workspace, workspace_bytes, fmlp_linear_w4_workspace_size(M, K, N, group)));
   if (M == 0) return ok();
   int cus = 0;
   TRY(check_device(&cus));
-  const W4Layer L{x, Wq, scales, zeros, nullptr, nullptr, nullptr, b, y, K, N, group, act, records_at(workspace, kHeader)};
+  const W4Layer L{x, Wq, scales, zeros, nullptr, nullptr, nullptr, b, y, K, N, group, act, scratch_at(workspace, kHeader), nullptr};
   return launched(launch_decode_w4(L, (int)M, cus, static_cast<hipStream_t>(stream)), "linear (4-bit weights) launch");
 }
 
 size_t fmlp_glu_w4_workspace_size(int64_t M, int64_t D, int64_t H, int group) {
   if (!w4_sizes_ok(M, D, group) || !w4_sizes_ok(M, H, group)) return 0;
   return kHeader + ws_bf16(M, H) +
-         std::max(decode_w4_records_bytes(M, D, group, true), decode_w4_records_bytes(M, H, group, false));
+         std::max(decode_w4_scratch_bytes(M, D, H, group, true), decode_w4_scratch_bytes(M, H, D, group, false));
 }
 
 fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16* sg, const fmlp_bf16* zg,
@@ -93,9 +93,9 @@ fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16*
   TRY(check_device(&cus));
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint16_t* m = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kHeader);
-  uint8_t* records = records_at(workspace, kHeader + ws_bf16(M, H));   // of x, then of m
-  const W4Layer L1{x, Wgq, sg, zg, Wuq, su, zu, nullptr, m, D, H, group, gate_act, records};
-  const W4Layer L2{m, Wdq, sd, zd, nullptr, nullptr, nullptr, nullptr, y, H, D, group, FMLP_ACT_NONE, records};
+  uint8_t* scratch = scratch_at(workspace, kHeader + ws_bf16(M, H));   // of the first layer, then of the second
+  const W4Layer L1{x, Wgq, sg, zg, Wuq, su, zu, nullptr, m, D, H, group, gate_act, scratch, nullptr};
+  const W4Layer L2{m, Wdq, sd, zd, nullptr, nullptr, nullptr, nullptr, y, H, D, group, FMLP_ACT_NONE, scratch, nullptr};
   HIP_TRY(launch_decode_w4(L1, (int)M, cus, s), "glu (4-bit weights) gate+up launch");
   return launched(launch_decode_w4(L2, (int)M, cus, s), "glu (4-bit weights) down launch");
 }

@@ -396,15 +396,16 @@ size_t fmlp_w8_workspace_size(int64_t M, int64_t H);
  * (FMLP_E_ALIGN), scales and zeros are finite, and a gated block has zero points
  * for both or neither of its gate and up weights (FMLP_E_ARG).  A token that
  * holds an infinity or a NaN gets outputs that are not finite; other tokens do
- * not see it.  One launch per layer, and a small one before it where M and the
- * layer's contraction are too large for LDS; deterministic.  The workspaces
+ * not see it.  One launch per layer, with a small one before it where M times
+ * the layer's contraction is large and one after it where that is too large for
+ * LDS; deterministic.  The workspaces
  * (fmlp_linear_w4: NULL where its size is 0) need no initialisation and leave
  * the first 8192 bytes alone.
  */
 fmlp_status fmlp_linear_w4(const fmlp_bf16* x, const uint8_t* Wq, const fmlp_bf16* scales, const fmlp_bf16* zeros,
                            const fmlp_bf16* b, int act, int64_t M, int64_t K, int64_t N, int group, fmlp_bf16* y,
                            void* workspace, size_t workspace_bytes, fmlp_stream stream);
-size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int group);
+size_t fmlp_linear_w4_workspace_size(int64_t M, int64_t K, int64_t N, int group);
 fmlp_status fmlp_glu_w4(const fmlp_bf16* x, const uint8_t* Wgq, const fmlp_bf16* sg, const fmlp_bf16* zg,
                         const uint8_t* Wuq, const fmlp_bf16* su, const fmlp_bf16* zu, const uint8_t* Wdq,
                         const fmlp_bf16* sd, const fmlp_bf16* zd, int gate_act, int64_t M, int64_t D, int64_t H,

@@ -151,14 +151,18 @@ def test_glu_w4_validation(L, kw, status, msg):
 
 
 def test_w4_sizes_and_no_tokens(L):
-    # activations that fit in LDS need no scratch; 16 tokens: 32 slots of 128, 32 exponents and 16 sums a group, per chunk
-    assert L.fmlp_linear_w4_workspace_size(4, 4096, 64) == 0
-    assert L.fmlp_linear_w4_workspace_size(16, 4096, 64) == 8192 + 32 * (4096 + 32 + 2 * 64)
-    assert L.fmlp_linear_w4_workspace_size(16, 4128, 32) == 8192 + 33 * (4096 + 32 + 4 * 64)
-    assert L.fmlp_linear_w4_workspace_size(0, 4096, 64) == 0 and L.fmlp_linear_w4_workspace_size(4, 4096, 48) == 0
+    # up to 256 records (tokens x chunks of 128) are made inside the kernel and need no scratch
+    assert L.fmlp_linear_w4_workspace_size(4, 8192, 64, 64) == 0
+    # records of 16 tokens: 32 slots of 128 bytes, 32 exponents, 16 sums a group; they fit in LDS together
+    assert L.fmlp_linear_w4_workspace_size(16, 4096, 64, 64) == 8192 + 32 * (4096 + 32 + 2 * 64)
+    assert L.fmlp_linear_w4_workspace_size(16, 4096, 64, 32) == 8192 + (32 * (4096 + 32 + 4 * 64) + 255) // 256 * 256
+    # two slices of 32 chunks, and the slices' fp32 sums of 16 x 72
+    assert L.fmlp_linear_w4_workspace_size(16, 8192, 72, 64) == 8192 + 64 * (4096 + 32 + 2 * 64) + 2 * 16 * 72 * 4
+    assert L.fmlp_linear_w4_workspace_size(0, 4096, 64, 64) == 0 and L.fmlp_linear_w4_workspace_size(4, 4096, 64, 48) == 0
     assert L.fmlp_glu_w4_workspace_size(4, 256, 128, 64) == 8192 + 1024
     assert L.fmlp_glu_w4_workspace_size(0, 256, 128, 64) == 0 and L.fmlp_glu_w4_workspace_size(17, 256, 128, 64) == 0
-    assert L.fmlp_glu_w4_workspace_size(16, 4096, 14336, 64) == 8192 + 16 * 14336 * 2 + 112 * (4096 + 32 + 2 * 64)
+    # the larger of the layers' scratch: H = 14336 in 4 slices of 28 chunks for the second
+    assert L.fmlp_glu_w4_workspace_size(16, 4096, 14336, 64) == 8192 + 16 * 14336 * 2 + 112 * (4096 + 32 + 2 * 64) + 4 * 16 * 4096 * 4
     assert w4(L, M=0, x=None, y=None) == OK
     assert glu_w4(L, M=0, x=None, y=None, ws=None, nb=0) == OK
     assert w4(L, M=0, x=None, y=None, q=None) == E_NULL
