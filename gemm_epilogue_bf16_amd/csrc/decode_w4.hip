@@ -292,7 +292,6 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
 
   const uint32_t wlane = (uint32_t)(r * (K / 2) + g * 16);
   const uint32_t slane = (uint32_t)(r * groups) * 2u;
-  constexpr int kRed = kWaves * NS * 64 * 16;   // the partial sums of a tile
   // the lane's slot (rows without a token read slot 0; their results are not used)
   const int slot = M8 ? ((r & 7) < M ? (r & 7) + (r >> 3) * M : 0) : (r < M ? r : 0);
   const int xop = g * (R.slots * 16) + slot * 16;    // the lane's operand bytes in a record, first half
@@ -400,12 +399,11 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
   // One output of a tile per thread o < 256: weight row o % 16, token
   // 4 ((o / 16) % 4) + (o / 64) % 4.
   const int ov = (threadIdx.x >> 6) & 3, om = 4 * g + ov;
-  // A finished tile: the waves' partial sums, added in wave order.  Two tiles'
-  // sums alternate in LDS, so one barrier a tile is enough: a wave writes a
-  // tile's sums after the barrier that every reader of those two tiles before
-  // has reached.
-  auto finish = [&](int tile, int parity, float bias) {
-    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + chunks * R.bytes + parity * kRed);   // [wave][stream][lane]
+  // A finished tile: the waves' partial sums, added in wave order.  (Two
+  // buffers with one barrier a tile took LDS from the records, a third slice of
+  // k at 16 tokens and K = 8192, and measured no faster.)
+  auto finish = [&](int tile, float bias) {
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + chunks * R.bytes);   // [wave][stream][lane]
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       red[(wave * NS + s) * 64 + lane] = tot[s];
@@ -433,10 +431,11 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
         L.y[(int64_t)om * L.N + n] = __builtin_bit_cast(uint16_t, ob);
       }
     }
+    lds_barrier();   // the sums are read before the next tile's are written
   };
 
   B A, C;
-  int ct = first, cs = 0, parity = 0;   // tile and step being consumed
+  int ct = first, cs = 0;   // tile and step being consumed
   // A step's weights are multiplied and their registers take those of the step
   // after the next.
   auto step = [&](B& now) {
@@ -445,8 +444,7 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
     const float bias = DUAL ? 0.f : __uint_as_float(now.bias << 16);
     issue(now);   // past the last step: descriptors of no rows, nothing is read
     if (++cs == steps) {
-      finish(ct, parity, bias);
-      parity ^= 1;
+      finish(ct, bias);
       cs = 0;
       ct += cut.per_slice;
     }
@@ -512,7 +510,7 @@ constexpr int64_t kLdsMax = 160 * 1024;   // of a block, one a CU
 constexpr int kUnitsInside = 256;         // tokens x chunks whose records a block makes itself
 
 int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
-int64_t red_bytes(bool dual) { return 2 * (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
+int64_t red_bytes(bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
 
 // The k slices of a call: as few as have records that fit in LDS, of equal
 // numbers of chunks (a multiple of 4, so that every slice starts on whole steps).

@@ -165,7 +165,7 @@ static_assert(m32_reads_conflict_free<8>(false) && m32_reads_conflict_free<8>(tr
 // k-major operand tiles (the backward's contractions over the rows of both
 // operands, read without a transpose copy).  A stage holds 64 k-rows of the
 // tile's 256 columns: rows of 512 bytes, 32 chunks of 16 B, chunk c of row k
-// at slot c ^ kswz(k).  A fragment (16 columns x 32 k) is two transposing
+// at slot c ^ kswz(k) (128 columns: rows of 256 bytes, 16 chunks).  A fragment (16 columns x 32 k) is two transposing
 // reads (ds_read_b64_tr_b16): within each 16-lane group, lane 4 r + q points
 // at 4 consecutive columns of k-row kbase + r, and lane j gets column group
 // j / 4, element j % 4 of all four rows, i.e. 4 consecutive k of one column;
@@ -279,7 +279,7 @@ __device__ __forceinline__ void ckpt_decode(const uint32_t code[2], uint32_t e12
 // grouped products with a bias of their own per group, ragged weight gradients.
 template <int OUT, bool GROUPED, int KM>
 constexpr bool gemm_is_train() {
-  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & kKmajorRagged) != 0 ||
+  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & (kKmajorRagged | kSplitC | kSplitB)) != 0 ||
          (GROUPED && (OUT == GEMM_OUT_BF16 || OUT == GEMM_OUT_DACT));
 }
 template <int OUT, bool GROUPED, int KM>
@@ -295,7 +295,7 @@ using gemm_params_t =
 // per MFMA) instead of v_mfma_f32_16x16x32_bf16: half the MFMA instructions
 // and half the operand register reads per flop, the same LDS bytes.
 // KM: bit 0 A, bit 1 B stored k-major, bit 2 a k range of its own for every
-// group (GemmParams::kmajor).
+// group, bit 3 two outputs, bit 4 two padded right operands (GemmParams::kmajor).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int R, int OUT, bool GATHER, bool GROUPED,
           int GACT = ACT_NONE, bool M32 = false, int KM = 0>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64)
@@ -330,9 +330,9 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   constexpr bool KMA = (KM & 1) != 0, KMB = (KM & 2) != 0;
   constexpr bool RAGK = (KM & kKmajorRagged) != 0;
   constexpr bool TRAIN = gemm_is_train<OUT, GROUPED, KM>();
-  static_assert(KM == 0 || (!DUAL && !GATHER && !M32 && (BM == 256 || !KMA) && BN == 256 && BK == 64 &&
-                            WAVES_M == 2 && WAVES_N == 4),
-                "k-major operands: tiles of 8 waves, 256 wide along a k-major operand, 16x16x32 MFMAs, one weight set");
+  static_assert(KM == 0 || (!DUAL && !GATHER && !M32 && BM % 128 == 0 && BN % 128 == 0 && BM <= 256 && BN <= 256 &&
+                            BK == 64 && (TM == 64 || TM == 128) && TN == 64),
+                "k-major operands: tiles of 128 or 256 columns, wave tiles 64 wide, 16x16x32 MFMAs, one weight set");
   static_assert(!GROUPED || KM == 0 || KM == 2, "grouped rows: only the weights k-major");
   static_assert(!RAGK || (KMA && KMB && !GROUPED), "ragged k ranges: both operands k-major");
   static_assert(!(OUT == GEMM_OUT_GLU_SAVE && M32) && kCkptBlock == 32, "a checkpoint block is one run of 4 lane groups");
@@ -461,15 +461,18 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   // offsets of the lane's load 0 within a tile (load i adds a constant number of rows)
   const uint32_t a_lane = (uint32_t)ra * lda2 + (uint32_t)a_k * 2u;
   const uint32_t b_lane = (uint32_t)ra * K2 + (uint32_t)b_k * 2u;
-  // k-major: load i of this wave fills k-rows 16 i + 2 wave + lane / 32 of
-  // the stage (2 rows of 512 B per instruction), the lane's slot lane % 32 of
+  // k-major: a row of the stage has CR = columns / 8 chunks and one instruction
+  // fills 64 / CR of them (256 columns: 2 rows of 512 B); load i of this wave
+  // fills k-rows KR i + (64 / CR) wave + lane / CR, the lane's slot lane % CR of
   // its row holding chunk slot ^ kswz(row) (kswz reads row bits 0-3, the same
   // for every i)
-  const int kr0 = 2 * wave + (lane >> 5);
-  const uint32_t km_chunk = (uint32_t)(((lane & 31) ^ kswz(kr0)) * 16);
+  constexpr int CRA = BM / 8, CRB = BN / 8;
+  constexpr int KRA = 64 / CRA * NW, KRB = 64 / CRB * NW;   // k-rows between a wave's loads
+  static_assert(KM == 0 || (KRA % 16 == 0 && KRB % 16 == 0), "one chunk permutation per lane");
+  const int kra0 = 64 / CRA * wave + lane / CRA, krb0 = 64 / CRB * wave + lane / CRB;
   const uint32_t ldb2 = (uint32_t)(KMB ? p.ldb : 0) * 2u;
-  const uint32_t a_lane_km = (uint32_t)kr0 * lda2 + km_chunk;
-  const uint32_t b_lane_km = (uint32_t)kr0 * ldb2 + km_chunk;
+  const uint32_t a_lane_km = (uint32_t)kra0 * lda2 + (uint32_t)(((lane % CRA) ^ kswz(kra0)) * 16);
+  const uint32_t b_lane_km = (uint32_t)krb0 * ldb2 + (uint32_t)(((lane % CRB) ^ kswz(krb0)) * 16);
   i32x4_t da, db0, db1;
   uint32_t a_gat[GATHER ? A_INS : 1];   // gather: the lane's source-row offsets in this tile
   auto issue_tile = [&](const Tile& t) {
@@ -485,12 +488,16 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
                   : make_desc(reinterpret_cast<uint64_t>(p.A + t.row_begin * p.lda), (uint32_t)a_rows_here * lda2);
     const int n_here = (int)min((int64_t)OUT_N, N - t.n0);   // weight rows of each set in this tile
     if constexpr (KMB) {   // the tile's columns are columns n0 .. of B0 [K0, ldb] (and B1 [K - K0, ldb]), N wide
-      const int64_t k0rows = p.kb_split > 0 ? p.kb_split : (int64_t)t.kc;
+      int64_t k0rows = p.kb_split > 0 ? p.kb_split : (int64_t)t.kc;
+      if constexpr ((KM & kSplitB) != 0) k0rows = p.kb_rows;   // rows from there to the split load zeros
       db0 = make_desc(reinterpret_cast<uint64_t>(t.b0 + (RAGK ? t.k_begin * p.ldb : 0) + t.n0),
                       RAGK && t.kc <= 0 ? 0u : (uint32_t)(((k0rows - 1) * p.ldb + N - t.n0) * 2));
-      db1 = p.kb_split > 0 ? make_desc(reinterpret_cast<uint64_t>(t.b1 + t.n0),
-                                       (uint32_t)((((int64_t)Kc - p.kb_split - 1) * p.ldb + N - t.n0) * 2))
-                           : db0;
+      if constexpr ((KM & kSplitB) != 0)
+        db1 = make_desc(reinterpret_cast<uint64_t>(t.b1 + t.n0), (uint32_t)(((k0rows - 1) * p.ldb + N - t.n0) * 2));
+      else
+        db1 = p.kb_split > 0 ? make_desc(reinterpret_cast<uint64_t>(t.b1 + t.n0),
+                                         (uint32_t)((((int64_t)Kc - p.kb_split - 1) * p.ldb + N - t.n0) * 2))
+                             : db0;
     } else {
       db0 = make_desc(reinterpret_cast<uint64_t>(t.b0 + t.n0 * K), (uint32_t)n_here * K2);
       db1 = DUAL ? make_desc(reinterpret_cast<uint64_t>(t.b1 + t.n0 * K), (uint32_t)n_here * K2) : db0;
@@ -579,8 +586,8 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   auto dma = [&](int i, uint32_t base, const StageIssue& st) {
     if (i < A_INS) {
       if constexpr (KMA) {   // k-rows past K load zeros
-        const uint32_t off = a_lane_km + (uint32_t)(16 * i) * lda2;
-        asm_load_lds(da, base + (uint32_t)(i * NW) * 1024u, st.k0 + kr0 + 16 * i < (RAGK ? st.kc : Kc) ? off : kOutOfRange, st.kb_a);
+        const uint32_t off = a_lane_km + (uint32_t)(KRA * i) * lda2;
+        asm_load_lds(da, base + (uint32_t)(i * NW) * 1024u, st.k0 + kra0 + KRA * i < (RAGK ? st.kc : Kc) ? off : kOutOfRange, st.kb_a);
       } else {
         const uint32_t off = GATHER ? a_gat[GATHER ? i : 0] : a_lane + (uint32_t)(RPI * i * NW) * lda2;
         asm_load_lds(da, base + (uint32_t)(i * NW) * 1024u, st.a_in ? off : kOutOfRange, st.kb_a);
@@ -588,9 +595,9 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     } else {
       const int b = i - A_INS;
       if constexpr (KMB) {
-        const uint32_t off = b_lane_km + (uint32_t)(16 * b) * ldb2;
+        const uint32_t off = b_lane_km + (uint32_t)(KRB * b) * ldb2;
         asm_load_lds(st.b1 ? db1 : db0, base + (uint32_t)(BM * CH * 16 + b * NW * 1024),
-                     st.k0 + kr0 + 16 * b < (RAGK ? st.kc : Kc) ? off : kOutOfRange, st.kb_b);
+                     st.k0 + krb0 + KRB * b < (RAGK ? st.kc : Kc) ? off : kOutOfRange, st.kb_b);
       } else {
         const bool up = DUAL && RPI * (b * NW) >= BN / 2;   // compile-time per i
         const uint32_t off = b_lane + (uint32_t)((RPI * b * NW) % (DUAL ? BN / 2 : BN)) * K2;
@@ -642,31 +649,31 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   // k-major: the lane's byte offset in the operand's region for k-step 0,
   // half 0 (k-row 8 (lane / 16) + (lane % 16) / 4) and fragment 0.  The rest
   // are compile-time: k-step 1 is 32 rows on (the swizzle reads row bits 0-3:
-  // + 16384 bytes), half 1 is 4 rows on (row bit 2 set: swizzle bit 3 flips,
-  // XOR 128, then + 2048), and a fragment XORs chunk bits the lane's own part
+  // only + 32 rows), half 1 is 4 rows on (row bit 2 set: swizzle bit 3 flips,
+  // XOR 128, then + 4 rows), and a fragment XORs chunk bits the lane's own part
   // leaves zero (activation f: 2 f; weight f: 4 (f / 2), plus half chunk
   // f % 2).  One register per operand.
   uint32_t km_x = 0, km_w = 0;
   if constexpr (KM != 0) {
     const int kq = lane >> 4, s16 = lane & 15;
     const int row = 8 * kq + (s16 >> 2);
-    km_x = (uint32_t)(row * 512 + (((wm * 16 + ((s16 & 3) >> 1)) ^ kswz(row)) << 4) + ((s16 & 1) << 3));
-    km_w = (uint32_t)(BM * CH * 16 + row * 512 + (((wn * 8 + (s16 & 3)) ^ kswz(row)) << 4));
+    km_x = (uint32_t)(row * (2 * BM) + (((wm * (TM / 8) + ((s16 & 3) >> 1)) ^ kswz(row)) << 4) + ((s16 & 1) << 3));
+    km_w = (uint32_t)(BM * CH * 16 + row * (2 * BN) + (((wn * 8 + (s16 & 3)) ^ kswz(row)) << 4));
   }
-  auto km_pair = [&](const u32x4_t* sl, uint32_t a0, int ks, uint32_t half) -> u32x4_t {
-    const uint32_t b = lds_addr(sl) + (uint32_t)(16384 * ks) + half;
-    return lds_read_tr_pair(b + a0, b + ((a0 ^ 128u) + 2048u));
+  auto km_pair = [&](const u32x4_t* sl, uint32_t a0, uint32_t rowb, int ks, uint32_t half) -> u32x4_t {
+    const uint32_t b = lds_addr(sl) + 32u * rowb * (uint32_t)ks + half;   // rowb: bytes of an LDS row
+    return lds_read_tr_pair(b + a0, b + ((a0 ^ 128u) + 4u * rowb));
   };
   auto frag_x = [&](const u32x4_t* sl, int ks, int f) -> u32x4_t {
     if constexpr (KMA) {
-      return km_pair(sl, km_x ^ (uint32_t)(32 * f), ks, 0u);
+      return km_pair(sl, km_x ^ (uint32_t)(32 * f), 2 * BM, ks, 0u);
     } else {
       return sl[x_idx[ks] + f * MR * CH];
     }
   };
   auto frag_w = [&](const u32x4_t* sl, int ks, int f) -> u32x4_t {
     if constexpr (KMB) {   // the pair permutation: columns 32 (f / 2) + 8 g + 4 (f % 2) .. + 3, g = 0..3
-      return km_pair(sl, km_w ^ (uint32_t)(64 * (f >> 1)), ks, (uint32_t)(8 * (f & 1)));
+      return km_pair(sl, km_w ^ (uint32_t)(64 * (f >> 1)), 2 * BN, ks, (uint32_t)(8 * (f & 1)));
     } else {
       return sl[w_idx[ks] + w_delta(f, FN, BN, DUAL, M32) * CH];
     }
@@ -788,7 +795,14 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
           const int64_t n = t.n0 + wn * TN + run_col(q, lg);
           float dm[8];
           run_vals(i, q, 0, dm);
-          if (!(row_ok && n < N)) continue;
+          const int64_t np = p.ldc2 >> 1;   // columns of dg, and of du: N rounded up to a stage of the product that reads them
+          if (!(row_ok && n < np)) continue;
+          uint16_t* d2 = static_cast<uint16_t*>(p.C2) + lrow * p.ldc2 + n;
+          if (n >= N) {
+            gst16(d2, zero4());
+            gst16(d2 + np, zero4());
+            continue;
+          }
           const uint8_t* code = p.codes + lrow * 2 * N + n;
           const uint8_t* sc = p.qscale + lrow * 2 * nb + n / kCkptBlock;
           uint32_t cg[2], cu[2];
@@ -807,9 +821,8 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
             du[r] = dm[r] * a;
           }
           gst16(static_cast<uint16_t*>(p.C) + lrow * p.ldc + n, pack_bf16x8(m));
-          uint16_t* d2 = static_cast<uint16_t*>(p.C2) + lrow * p.ldc2 + n;
           gst16(d2, pack_bf16x8(dg));
-          gst16(d2 + N, pack_bf16x8(du));
+          gst16(d2 + np, pack_bf16x8(du));
         }
       } else if constexpr (OUT == GEMM_OUT_DGLU) {
         // recomputed g and u with the incoming dm: m for the down projection's
@@ -876,7 +889,13 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
 #pragma unroll
               for (int r = 0; r < 8; ++r) v[r] = act_of<ACT>(v[r]);
             }
-            gst16(static_cast<uint16_t*>(p.C) + (RAGK ? t.c_off : 0) + lrow * p.ldc + n, pack_bf16x8(v));
+            if constexpr ((KM & kSplitC) != 0) {   // rows from c_split on are C2's; either has c_rows
+              const bool second = lrow >= p.c_split;
+              const int64_t cr = lrow - (second ? p.c_split : 0);
+              if (cr < p.c_rows) gst16(static_cast<uint16_t*>(second ? p.C2 : p.C) + cr * p.ldc + n, pack_bf16x8(v));
+            } else {
+              gst16(static_cast<uint16_t*>(p.C) + (RAGK ? t.c_off : 0) + lrow * p.ldc + n, pack_bf16x8(v));
+            }
           }
         }
       }

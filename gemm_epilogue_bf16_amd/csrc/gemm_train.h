@@ -10,7 +10,8 @@ namespace fmlp {
 // Output kinds beyond GemmOut.
 constexpr int GEMM_OUT_GLU_SAVE = 5;     // GEMM_OUT_GEGLU that also writes g and u as E4M3 codes with block scales
 constexpr int GEMM_OUT_DGLU_SAVED = 6;   // acc = dm; g and u come from those codes: C = m = act(g) * u,
-                                         // C2 = [dm * u * act'(g) | dm * act(g)]
+                                         // C2 = [dm * u * act'(g) | dm * act(g)], each ldc2 / 2 columns
+                                         // wide (N and zeros)
 
 // Hidden units of one row that share a checkpoint scale.
 constexpr int kCkptBlock = 32;
@@ -20,21 +21,33 @@ constexpr int kCkptBlock = 32;
 // C[g] [M, N] = A[rows of g]^T . B[rows of g], zeros for a group without rows.
 constexpr int kKmajorRagged = 4;
 
+// bit 3: rows [0, c_rows) of the output go to C, rows [c_split, c_split + c_rows)
+// to C2 (bf16, both with row stride ldc), the others nowhere: two weight gradients
+// with the same right operand in one launch.
+constexpr int kSplitC = 8;
+// bit 4, with kb_split: B0 and B1 have kb_rows (at most kb_split) rows each, and
+// the k rows from there to the split (or to K) are zeros.
+constexpr int kSplitB = 16;
+
 struct GemmTrainParams : GemmParams {
   uint8_t* codes;              // checkpoint: E4M3 codes [rows, 2N], g in columns [0, N), u in [N, 2N)
   uint8_t* qscale;             // and scale exponents (+ 127) [rows, 2 ceil(N / kCkptBlock)]
   int64_t stride_bias;         // grouped: elements between consecutive groups' biases
+  int64_t c_split, c_rows;     // kSplitC
+  int64_t kb_rows;             // kSplitB
   int64_t stride_c;            // ragged: elements between consecutive groups' outputs
   const int64_t* work_off;     // ragged: [groups + 1] prefix of the stages of one tile of each group (see GroupPlan)
 };
 
+// Every form below runs on TILE_128x128 or TILE_256x256.
 // y = act(x W[g]^T + b[g]) over each group's rows (GEMM_OUT_BF16), its dz
-// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2).  tile:
-// TILE_128x128 or TILE_256x256; with kmajor = 2 TILE_128x128 stands for a
-// 128 x 256 tile (the k-major operand's tile is 256 columns wide).
+// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2).
 hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
-hipError_t launch_gemm_ragged(int out_kind, const GemmTrainParams& p, hipStream_t s);
+hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
+// Dense products with k-major operands on either tile, bf16 or split fp32:
+// kmajor = 2 | kSplitB, 3 or 3 | kSplitC (bf16 only).
+hipError_t launch_gemm_kmajor(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // GEMM_OUT_GLU_SAVE, and GEMM_OUT_DGLU_SAVED (kmajor 0 or 2).
 hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 

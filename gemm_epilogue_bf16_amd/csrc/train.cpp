@@ -42,12 +42,55 @@ GemmTrainParams train_params(const GemmParams& p) {
   return t;
 }
 
-// Row tiles of a grouped product.  256 rows need groups that fill them (the
-// rows are on the device: the mean of R / E stands for them) and enough tiles
-// for the chip; else 128.
-bool grouped_big(int64_t R, int64_t N, int32_t E, int cus) {
-  const int64_t tiles = (R / 256 + E / 2) * ((N + 255) / 256);
-  return R >= (int64_t)192 * E && tiles >= cus;
+// ---- tile and split of a product ------------------------------------------------
+// A product runs in rounds of one 256x256 tile per compute unit or two 128x128
+// ones, for as many 64-k stages as its longest tile has; splitting k in P parts
+// makes more, shorter tiles, and costs the parts' fp32 round trip and a launch.
+// The estimate of a candidate, in us, from times measured on the k-major forms
+// (a stage of a round, and what a tile costs beside its stages):
+constexpr double kStage256 = 1.50, kTile256 = 10.0;
+constexpr double kStage128 = 0.95, kTile128 = 6.0;
+constexpr double kPartsLaunch = 5.0, kPartsBytesPerUs = 4.0e6;
+constexpr int kPlanCus = 256;   // not the device's: workspaces are sized without one
+
+struct ProductPlan {
+  int tile, split;
+};
+// tiles256, tiles128: the product's tiles of either size, `stages` of 64 k each;
+// out: its output elements; max_split: 1 where k cannot be split.
+ProductPlan plan_product(int64_t tiles256, int64_t tiles128, int64_t stages, int64_t out, int max_split) {
+  ProductPlan best{TILE_256x256, 1};
+  double least = 0;
+  for (int P = 1; P <= max_split; ++P) {
+    if (P > 1 && stages / P < 4) break;
+    const double parts = P > 1 ? kPartsLaunch + 8.0 * P * (double)out / kPartsBytesPerUs : 0;
+    for (int tile : {TILE_256x256, TILE_128x128}) {
+      const bool big = tile == TILE_256x256;
+      const int64_t rounds = ((big ? tiles256 : tiles128) * P + (big ? 1 : 2) * kPlanCus - 1) / ((big ? 1 : 2) * kPlanCus);
+      const double t = (double)rounds * ((double)((stages + P - 1) / P) * (big ? kStage256 : kStage128) +
+                                         (big ? kTile256 : kTile128)) + parts;
+      if (least == 0 || t < least) {
+        least = t;
+        best = {tile, P};
+      }
+    }
+  }
+  return best;
+}
+int64_t tiles_of(int64_t rows, int64_t cols, int t) { return ((rows + t - 1) / t) * ((cols + t - 1) / t); }
+constexpr int kMaxSplit = 8;
+ProductPlan plan_dense(int64_t rows, int64_t cols, int64_t K, int max_split = kMaxSplit) {
+  return plan_product(tiles_of(rows, cols, 256), tiles_of(rows, cols, 128), (K + 63) / 64, rows * cols, max_split);
+}
+size_t parts_bytes(const ProductPlan& p, int64_t out) {
+  return p.split > 1 ? round_up((size_t)p.split * (size_t)out * 4, 256) : 0;
+}
+
+// The row tiles of E ragged groups: the sizes are on the device, so the mean
+// R / E stands for them, with half a tile wasted per group.
+bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
+  const int64_t t256 = (R / 256 + (E + 1) / 2) * ((N + 255) / 256), t128 = (R / 128 + (E + 1) / 2) * ((N + 127) / 128);
+  return plan_product(t256, t128, (K + 63) / 64, R * N, 1).tile == TILE_256x256;
 }
 
 void set_groups(GemmTrainParams& p, const GroupPlan& plan, int32_t E, int64_t R, bool big) {
@@ -58,27 +101,23 @@ void set_groups(GemmTrainParams& p, const GroupPlan& plan, int32_t E, int64_t R,
   p.tiles_m = (int)(R / bm + E);   // at most one partial tile per group
 }
 
-// Parts of the rows that a weight gradient is split in, as for the dense one:
-// when all groups' tiles leave compute units idle.
-int grouped_split(int64_t R, int64_t N, int64_t K, int32_t E) {
-  const int64_t tiles = ((N + 255) / 256) * ((K + 255) / 256) * E;
-  if (tiles >= 256) return 1;
-  const int64_t P = std::min<int64_t>({256 / tiles, 8, R / E / 512});
-  return P > 1 ? (int)P : 1;
+// The weight gradient of E groups: each its own rows, the mean stands for them.
+ProductPlan plan_grouped_dw(int64_t R, int64_t N, int64_t K, int32_t E) {
+  return plan_product(E * tiles_of(N, K, 256), E * tiles_of(N, K, 128), (R / E + 63) / 64, E * N * K, kMaxSplit);
 }
 
 struct GroupedBwdLayout {
   PlanLayout plan;
   size_t dz, parts, total;
-  int split;
+  ProductPlan dw;
 };
 GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, int act) {
   GroupedBwdLayout L;
   L.plan = plan_layout(E);
-  L.split = grouped_split(R, N, K, E);
+  L.dw = plan_grouped_dw(R, N, K, E);
   size_t o = L.plan.end;
   L.dz = o;    o += act != FMLP_ACT_NONE ? ws_bf16(R, N) : 0;
-  L.parts = o; o += L.split > 1 ? round_up((size_t)L.split * (size_t)E * (size_t)N * (size_t)K * 4, 256) : 0;
+  L.parts = o; o += parts_bytes(L.dw, E * N * K);
   L.total = o;
   return L;
 }
@@ -111,7 +150,7 @@ fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, co
   TRY(check_device(&cus));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const GroupPlan plan = plan_at(workspace, L);
-  const bool big = grouped_big(R, N, E, cus);
+  const bool big = grouped_big(R, N, K, E);
   HIP_TRY(launch_group_plan(group_off, R, E, big ? 256 : 128, 1, plan, s), "grouped_linear plan launch");
   GemmTrainParams p = train_params(dense_params(x, K, W, nullptr, b, y, N, R, N, K, act, cus));
   set_groups(p, plan, E, R, big);
@@ -159,9 +198,9 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
   char* ws = static_cast<char*>(workspace);
   const GroupPlan plan = plan_at(workspace, L.plan);
   // one plan serves dz and dx: both run on row tiles of the same height
-  const bool big = grouped_big(R, K, E, cus);
+  const bool big = grouped_big(R, K, N, E);
   const int tile = big ? TILE_256x256 : TILE_128x128;
-  HIP_TRY(launch_group_plan(group_off, R, E, big ? 256 : 128, L.split, plan, s), "grouped_linear_bwd plan launch");
+  HIP_TRY(launch_group_plan(group_off, R, E, big ? 256 : 128, L.dw.split, plan, s), "grouped_linear_bwd plan launch");
   const uint16_t* dz = dy;
   if (act != FMLP_ACT_NONE) {   // dz = dy * act'(x W^T + b), z recomputed
     uint16_t* dzw = reinterpret_cast<uint16_t*>(ws + L.dz);
@@ -184,7 +223,7 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
   }
   {   // dW[e] = dz^T x over the group's rows, both read k-major
     float* parts = reinterpret_cast<float*>(ws + L.parts);
-    const bool split = L.split > 1;
+    const bool split = L.dw.split > 1;
     GemmTrainParams p = train_params(dense_params(dz, N, x, nullptr, nullptr, split ? static_cast<void*>(parts) : dW, K, N,
                                                   K, R, FMLP_ACT_NONE, cus));
     p.kmajor = 3 | kKmajorRagged;
@@ -194,11 +233,11 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
     p.groups = E;
     p.stride_c = N * K;
     if (split) {
-      p.ksplit = L.split;
+      p.ksplit = L.dw.split;
       p.c_kstride = E * N * K;
     }
-    HIP_TRY(launch_gemm_ragged(split ? GEMM_OUT_F32_SCALED : GEMM_OUT_BF16, p, s), "grouped_linear_bwd dW launch");
-    if (split) HIP_TRY(launch_sum_parts(parts, L.split, E * N * K, E * N * K, dW, s), "grouped_linear_bwd dW sum");
+    HIP_TRY(launch_gemm_ragged(split ? GEMM_OUT_F32_SCALED : GEMM_OUT_BF16, L.dw.tile, p, s), "grouped_linear_bwd dW launch");
+    if (split) HIP_TRY(launch_sum_parts(parts, L.dw.split, E * N * K, E * N * K, dW, s), "grouped_linear_bwd dW sum");
   }
   if (db) HIP_TRY(launch_group_colsum(dz, plan.group_off, E, N, db, s), "grouped_linear_bwd db launch");
   return ok();
@@ -246,19 +285,57 @@ fmlp_status fmlp_glu_ckpt(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf
 }
 
 namespace {
-// m and [dg | du], then scratch that the steps use in turn: Wd^T for dm; the
-// transposes of glu_bwd_products; the split weight gradients' parts.
+// The products of the checkpoint's backward, all with operands as stored (read
+// k-major): dm [M, H] over D, dx [M, D] over 2H, dWd [D, H] and dWg | dWu [2H, D]
+// over the tokens.  `stored`: the spans fit (operands below 2^30 elements);
+// else the transposing form of fmlp_glu_bwd's last steps.
+// dg and du are Hp columns wide, H rounded up to the 64-k stages of dx's product,
+// with zeros in between.
 struct CkptBwdLayout {
+  bool stored;
+  int64_t Hp;
+  ProductPlan dm, dx, dwd, dwgu;
   size_t m, dgdu, scratch, total;
 };
 CkptBwdLayout ckpt_bwd_layout(int64_t M, int64_t D, int64_t H) {
   CkptBwdLayout L;
+  L.Hp = (H + 63) / 64 * 64;
+  L.stored = D * L.Hp < kMaxSpan && M * D < kMaxSpan && 2 * M * L.Hp < kMaxSpan;
+  if (!L.stored) L.Hp = H;
+  L.dm = plan_dense(M, H, D, 1);   // its epilogue needs the whole sum
+  L.dx = plan_dense(M, D, 2 * L.Hp);
+  L.dwd = plan_dense(D, H, M);
+  L.dwgu = plan_dense(2 * L.Hp, D, M);
   size_t o = kHeader;
   L.m = o;       o += ws_bf16(M, H);
-  L.dgdu = o;    o += ws_bf16(M, 2 * H);
-  L.scratch = o; o += std::max(ws_bf16(H, D), glu_products_scratch(M, D, H));
+  L.dgdu = o;    o += ws_bf16(M, 2 * L.Hp);
+  L.scratch = o;   // the parts of split products, one at a time, or the transposes
+  o += L.stored ? std::max({parts_bytes(L.dx, M * D), parts_bytes(L.dwd, D * H), parts_bytes(L.dwgu, 2 * L.Hp * D)})
+                : std::max(ws_bf16(H, D), glu_products_scratch(M, D, H));
   L.total = o;
   return L;
+}
+// A product on its plan: C = A . B with the operands of `kmajor`; with C2, rows
+// [0, rows) of it are C's and rows [at, at + rows) C2's.
+hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, uint16_t* C2, int64_t at, int64_t rows,
+                       float* parts, hipStream_t s) {
+  if (plan.split == 1) {
+    p.C = C;
+    if (C2) {
+      p.C2 = C2;
+      p.c_split = at;
+      p.c_rows = rows;
+      p.kmajor |= kSplitC;
+    }
+    return launch_gemm_kmajor(GEMM_OUT_BF16, plan.tile, p, s);
+  }
+  p.C = parts;
+  p.ksplit = plan.split;
+  p.c_kstride = p.M * p.N;
+  hipError_t e = launch_gemm_kmajor(GEMM_OUT_F32_SCALED, plan.tile, p, s);
+  if (e == hipSuccess) e = launch_sum_parts(parts, plan.split, p.M * p.N, (C2 ? rows : p.M) * p.N, C, s);
+  if (e == hipSuccess && C2) e = launch_sum_parts(parts + at * p.N, plan.split, p.M * p.N, rows * p.N, C2, s);
+  return e;
 }
 }  // namespace
 
@@ -307,19 +384,36 @@ fmlp_status fmlp_glu_ckpt_bwd(const fmlp_bf16* x, const fmlp_fp8* codes, const u
   // [dg | du]; dm stays in registers.  The contraction runs over Wd's rows.
   GemmTrainParams p = train_params(dense_params(dy, D, Wd, nullptr, nullptr, m, H, M, H, D, gate_act, cus));
   p.C2 = dgdu;
-  p.ldc2 = 2 * H;
+  p.ldc2 = 2 * L.Hp;
   p.codes = const_cast<fmlp_fp8*>(codes);
   p.qscale = const_cast<uint8_t*>(scales);
-  if (gemm_bkmajor_ok(M, H, D, 0, cus)) {
-    p.kmajor = 2;
-    p.ldb = H;
-    HIP_TRY(launch_gemm_ckpt(GEMM_OUT_DGLU_SAVED, TILE_256x256, p, s), "glu_ckpt_bwd dm launch");
-  } else {
+  if (!L.stored) {
     HIP_TRY(launch_transpose(Wd, D, H, H, scratch, D, D, s), "glu_ckpt_bwd transpose Wd");
     p.B0 = scratch;
     HIP_TRY(launch_gemm_ckpt(GEMM_OUT_DGLU_SAVED, TILE_128x128, p, s), "glu_ckpt_bwd dm launch");
+    return glu_bwd_products(x, dy, Wg, Wu, m, dgdu, M, D, H, dx, dWg, dWu, dWd, scratch, cus, s);
   }
-  return glu_bwd_products(x, dy, Wg, Wu, m, dgdu, M, D, H, dx, dWg, dWu, dWd, scratch, cus, s);
+  p.kmajor = 2;
+  p.ldb = H;
+  HIP_TRY(launch_gemm_ckpt(GEMM_OUT_DGLU_SAVED, L.dm.tile, p, s), "glu_ckpt_bwd dm launch");
+  float* parts = reinterpret_cast<float*>(scratch);
+  // dx = [dg | du] [Wg ; Wu]: one product over 2 Hp
+  GemmTrainParams q = train_params(dense_params(dgdu, 2 * L.Hp, Wg, Wu, nullptr, nullptr, D, M, D, 2 * L.Hp, FMLP_ACT_NONE, cus));
+  q.kmajor = 2 | kSplitB;
+  q.ldb = D;
+  q.kb_split = L.Hp;
+  q.kb_rows = H;
+  HIP_TRY(run_product(L.dx, q, dx, nullptr, 0, 0, parts, s), "glu_ckpt_bwd dx launch");
+  q = train_params(dense_params(dy, D, m, nullptr, nullptr, nullptr, H, D, H, M, FMLP_ACT_NONE, cus));
+  q.kmajor = 3;
+  q.ldb = H;
+  HIP_TRY(run_product(L.dwd, q, dWd, nullptr, 0, 0, parts, s), "glu_ckpt_bwd dWd launch");
+  // dWg | dWu = [dg | du]^T x: one product of 2 Hp rows
+  q = train_params(dense_params(dgdu, 2 * L.Hp, x, nullptr, nullptr, nullptr, D, 2 * L.Hp, D, M, FMLP_ACT_NONE, cus));
+  q.kmajor = 3;
+  q.ldb = D;
+  HIP_TRY(run_product(L.dwgu, q, dWg, dWu, L.Hp, H, parts, s), "glu_ckpt_bwd dWg, dWu launch");
+  return ok();
 }
 
 }  // extern "C"
