@@ -164,12 +164,11 @@ def lib() -> ctypes.CDLL:
         L.fmlp_glu_ckpt.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]
         L.fmlp_glu_ckpt_bwd.argtypes = [_p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p,
                                         _sz, _p]
-        L.fmlp_grouped_linear.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _p, _p, _sz, _p]
+        L.fmlp_grouped_linear.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _p, _p]
         L.fmlp_grouped_linear_bwd.argtypes = [_p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, ctypes.c_int32, _p, _p,
                                               _p, _p, _sz, _p]
         for f, a in (("fmlp_glu_ckpt_workspace_size", [_i64] * 3), ("fmlp_glu_ckpt_bwd_workspace_size", [_i64] * 3),
                      ("fmlp_glu_ckpt_codes_size", [_i64] * 2), ("fmlp_glu_ckpt_scales_size", [_i64] * 2),
-                     ("fmlp_grouped_linear_workspace_size", [ctypes.c_int32]),
                      ("fmlp_grouped_linear_bwd_workspace_size", [_i64] * 3 + [ctypes.c_int32, ctypes.c_int])):
             getattr(L, f).argtypes = a
             getattr(L, f).restype = _sz
@@ -558,28 +557,25 @@ def _grouped_args(x, group_off, W, b):
     return R, K, N, E
 
 
-def _grouped_linear_call(x, group_off, W, b, act, out, workspace):
+def _grouped_linear_call(x, group_off, W, b, act, out):
     R, K, N, E = _grouped_args(x, group_off, W, b)
     y = _out("out", out, (R, N), x)
-    L = lib()
-    ws = _scratch(x, workspace, L.fmlp_grouped_linear_workspace_size(E))
-    return BoundCall(L.fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K,
-                                             N, E, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device)),
-                     y, (x, group_off, W, b, ws))
+    return BoundCall(lib().fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K,
+                                                 N, E, y.data_ptr(), _stream(x.device)), y, (x, group_off, W, b))
 
 
-def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None):
+def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None):
     """y[r] = act(x[r] W[e]^T + b[e]) for the rows [group_off[e], group_off[e+1]) of every group e.
 
     x [R, K]; group_off int32 [E + 1] on the device; W [E, N, K]; b [E, N] or None -> y [R, N].  Rows outside every
     group are not written: with out=None they hold whatever the new tensor held."""
     with torch.cuda.device(x.device):
-        return _grouped_linear_call(x, group_off, W, b, act, out, workspace)()
+        return _grouped_linear_call(x, group_off, W, b, act, out)()
 
 
-def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None) -> BoundCall:
+def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None) -> BoundCall:
     with torch.cuda.device(x.device):
-        return _grouped_linear_call(x, group_off, W, b, act, out, workspace)
+        return _grouped_linear_call(x, group_off, W, b, act, out)
 
 
 def _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace):

@@ -286,6 +286,69 @@ template <int OUT, bool GROUPED, int KM>
 using gemm_params_t =
     typename std::conditional<gemm_is_train<OUT, GROUPED, KM>(), GemmTrainParams, GemmParams>::type;
 
+// ---------------------------------------------------------------------------
+// Groups of the grouped and ragged products
+// ---------------------------------------------------------------------------
+// What a block knows about its groups, made from the caller's offsets at its
+// start: offsets clamped into [0, R] and to a running maximum (a bad table gives
+// wrong rows, never an access outside the buffers), the prefix of the groups'
+// row tiles, and for ragged products the prefix of one tile's 64-k stages.  One
+// wave scans 64 groups at a time (under 1 us for 64 groups); a table made once
+// by a kernel of its own cost a launch (4.6 us), and searching it in memory a
+// round trip per halving, per tile.
+template <bool RAGGED>
+struct GroupTables {
+  int32_t off[kMaxGroups + 1];
+  int32_t tile[RAGGED ? 1 : kMaxGroups + 1];
+  int64_t work[RAGGED ? kMaxGroups + 1 : 1];
+};
+template <class T, class Op>
+__device__ __forceinline__ T wave_scan(T v, int lane, Op op) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const T o = __shfl_up(v, d, 64);
+    if (lane >= d) v = op(o, v);
+  }
+  return v;
+}
+// Called by every thread of the block.  bm: rows of a tile; split: parts of a
+// ragged product's k range (a tile costs at least one stage for each).
+template <bool RAGGED>
+__device__ __forceinline__ void make_group_tables(GroupTables<RAGGED>& t, const int32_t* off, int groups, int32_t R, int bm,
+                                                  int split) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int32_t end0 = min(max(off[0], 0), R);   // the previous 64 groups' end, tiles and stages
+    int32_t tile0 = 0;
+    int64_t work0 = 0;
+    if (lane == 0) {
+      t.off[0] = end0;
+      t.tile[0] = 0;
+      t.work[0] = 0;
+    }
+    for (int base = 0; base < groups; base += 64) {
+      const int g = base + lane;
+      const int32_t mine = g < groups ? min(max(off[g + 1], end0), R) : end0;
+      const int32_t end = wave_scan(mine, lane, [](int32_t a, int32_t b) { return max(a, b); });
+      int32_t begin = __shfl_up(end, 1, 64);
+      if (lane == 0) begin = end0;
+      const int32_t rows = end - begin;   // 0 past the last group
+      if (g < groups) t.off[g + 1] = end;
+      if constexpr (RAGGED) {
+        const int64_t w = work0 + wave_scan((int64_t)max((rows + 63) / 64, split), lane, [](int64_t a, int64_t b) { return a + b; });
+        if (g < groups) t.work[g + 1] = w;
+        work0 = __shfl(w, 63, 64);
+      } else {
+        const int32_t n = tile0 + wave_scan((rows + bm - 1) / bm, lane, [](int32_t a, int32_t b) { return a + b; });
+        if (g < groups) t.tile[g + 1] = n;
+        tile0 = __shfl(n, 63, 64);
+      }
+      end0 = __shfl(end, 63, 64);
+    }
+  }
+  __syncthreads();
+}
+
 // GACT: the gate activation of a gated (GEMM_OUT_GEGLU, GEMM_OUT_DGLU) kernel,
 // or the activation of a GEMM_OUT_DACT kernel, fixed per kernel so each
 // carries one epilogue: with several epilogue copies behind a
@@ -350,13 +413,20 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   const int li = lane & (MR - 1);   // fragment row (weight) / column (activation)
   const int lg = lane / MR;         // k group: 8 consecutive k
 
+  constexpr bool OWN_TABLES = RAGK || (GROUPED && TRAIN);
+  __shared__ typename std::conditional<OWN_TABLES, GroupTables<RAGK>, int>::type tables;
+  if constexpr (OWN_TABLES)
+    make_group_tables(tables, p.group_off, p.groups, (int32_t)p.group_rows, BM, RAGK && p.ksplit > 1 ? p.ksplit : 1);
+
   // ---- this block's tiles ----------------------------------------------------
   // The grid is persistent (at most one block per CU).  Logical tiles (in
   // grouped order) are split into one contiguous range per XCD, in
   // proportion to its blocks, and the blocks of an XCD take its range
   // round-robin, so at any time the blocks sharing an L2 work on
   // neighbouring tiles.  Grouped mode counts only the tiles that exist.
-  const int tiles_m = GROUPED ? p.tile_off[p.groups] : p.tiles_m;
+  auto group_off = [&](int g) -> int { if constexpr (OWN_TABLES) return tables.off[g]; else return p.group_off[g]; };
+  auto tile_off = [&](int g) -> int { if constexpr (OWN_TABLES) return tables.tile[g]; else return p.tile_off[g]; };
+  const int tiles_m = GROUPED ? __builtin_amdgcn_readfirstlane(tile_off(p.groups)) : p.tiles_m;
   // split-K (fp32 output only): every tile appears KSP times, once per part
   // of the K range, each writing its own output copy
   constexpr bool SPLITK = OUT == GEMM_OUT_F32_SCALED;
@@ -376,13 +446,13 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     const int64_t nb = blocks_before(x);
     if constexpr (RAGK) {
       const int64_t tt = (int64_t)tiles_m * p.tiles_n;
-      const int64_t w = p.work_off[p.groups] * tt * nb / G;   // in stages
+      const int64_t w = tables.work[p.groups] * tt * nb / G;   // in stages
       int lo = 0, hi = p.groups;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.work_off[mid] * tt <= w) lo = mid; else hi = mid;
+        if (tables.work[mid] * tt <= w) lo = mid; else hi = mid;
       }
-      const int64_t in = (w - p.work_off[lo] * tt) * KSP / (p.work_off[lo + 1] - p.work_off[lo]);
+      const int64_t in = (w - tables.work[lo] * tt) * KSP / (tables.work[lo + 1] - tables.work[lo]);
       return (int)(lo * tt * KSP + in);
     } else {
       return (int)((int64_t)total * nb / G);
@@ -415,18 +485,18 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     t.c_off = 0;
     t.kc = Kc;
     if constexpr (RAGK) {
-      t.k_begin = p.group_off[lg_t];
-      t.kc = p.group_off[lg_t + 1] - p.group_off[lg_t];
+      t.k_begin = group_off(lg_t);
+      t.kc = group_off(lg_t + 1) - group_off(lg_t);
       t.c_off = (int64_t)lg_t * p.stride_c;
     }
     if constexpr (GROUPED) {
       int lo = 0, hi = p.groups;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.tile_off[mid] <= tm) lo = mid; else hi = mid;
+        if (tile_off(mid) <= tm) lo = mid; else hi = mid;
       }
-      t.row_begin = (int64_t)p.group_off[lo] + (int64_t)(tm - p.tile_off[lo]) * BM;
-      t.row_end = min(t.row_begin + BM, (int64_t)p.group_off[lo + 1]);
+      t.row_begin = (int64_t)group_off(lo) + (int64_t)(tm - tile_off(lo)) * BM;
+      t.row_end = min(t.row_begin + BM, (int64_t)group_off(lo + 1));
       t.b0 += (int64_t)lo * p.strideB;
       if constexpr (TRAIN) {
         if (p.bias) t.bias += (int64_t)lo * p.stride_bias;

@@ -20,6 +20,7 @@ constexpr int kCkptBlock = 32;
 // and every group has its own range of k rows, [group_off[g], group_off[g+1]):
 // C[g] [M, N] = A[rows of g]^T . B[rows of g], zeros for a group without rows.
 constexpr int kKmajorRagged = 4;
+constexpr int kMaxGroups = 1024;
 
 // bit 3: rows [0, c_rows) of the output go to C, rows [c_split, c_split + c_rows)
 // to C2 (bf16, both with row stride ldc), the others nowhere: two weight gradients
@@ -36,7 +37,7 @@ struct GemmTrainParams : GemmParams {
   int64_t c_split, c_rows;     // kSplitC
   int64_t kb_rows;             // kSplitB
   int64_t stride_c;            // ragged: elements between consecutive groups' outputs
-  const int64_t* work_off;     // ragged: [groups + 1] prefix of the stages of one tile of each group (see GroupPlan)
+  int64_t group_rows;          // grouped, ragged: the rows there are; group_off is the caller's table, unchecked
 };
 
 // Every form below runs on TILE_128x128 or TILE_256x256.
@@ -45,8 +46,8 @@ struct GemmTrainParams : GemmParams {
 hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
 hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
-// Dense products with k-major operands on either tile, bf16 or split fp32:
-// kmajor = 2 | kSplitB, 3 or 3 | kSplitC (bf16 only).
+// Dense products on either tile, bf16 or split fp32: kmajor = 0, 2 | kSplitB, 3 or
+// 3 | kSplitC (bf16 only).
 hipError_t launch_gemm_kmajor(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // GEMM_OUT_GLU_SAVE, and GEMM_OUT_DGLU_SAVED (kmajor 0 or 2).
 hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
@@ -54,19 +55,9 @@ hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hi
 // ---------------------------------------------------------------------------
 // Helpers of the grouped products (grouped.hip).
 // ---------------------------------------------------------------------------
-// What the kernels of a call read about its groups, made on the device from the
-// caller's offsets: clamped into [0, R] and made nondecreasing (a bad table
-// gives wrong rows, never an access outside the buffers), the prefix of the
-// groups' bm-row tiles, and the prefix of max(stages, split) 64-row stages.
-struct GroupPlan {
-  int32_t* group_off;   // [E + 1]
-  int32_t* tile_off;    // [E + 1]
-  int64_t* work_off;    // [E + 1]
-};
-hipError_t launch_group_plan(const int32_t* off, int64_t R, int E, int bm, int split, const GroupPlan& plan,
-                             hipStream_t s);
 // db[e, n] = bf16(sum of dz[r, n] over group e's rows), fp32, a fixed order.
-hipError_t launch_group_colsum(const uint16_t* dz, const int32_t* group_off, int E, int64_t N, uint16_t* db,
+// group_off: the caller's table for R rows, unchecked.
+hipError_t launch_group_colsum(const uint16_t* dz, const int32_t* group_off, int64_t R, int E, int64_t N, uint16_t* db,
                                hipStream_t s);
 
 }  // namespace fmlp

@@ -22,6 +22,7 @@ hipError_t by_act(int act, F f) {
 }  // namespace
 
 hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s) {
+  if (p.groups < 1 || p.groups > kMaxGroups) return hipErrorInvalidValue;
   const bool big = tile == TILE_256x256;
   if (!big && tile != TILE_128x128) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16 && p.kmajor == 2) {
@@ -32,16 +33,16 @@ hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p,
   if (p.kmajor != 0) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16)
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s)
-               : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s);
+               : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s);
   if (out_kind == GEMM_OUT_DACT)
     return by_act(p.act, [&](auto a) {
       return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s)
-                 : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_DACT, false, true, a.value>(p, s);
+                 : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s);
     });
   return hipErrorInvalidValue;
 }
 
-// k-major operands: 256x256 tiles of 8 waves, or 128x128 of 4 (two blocks a CU)
+// 256x256 tiles of 8 waves, or 128x128 of 4 (two blocks a CU), 64-k stages
 template <int OUT, int KM, bool GROUPED = false>
 static hipError_t launch_km(int tile, const gemm_params_t<OUT, GROUPED, KM>& p, hipStream_t s) {
   if (tile == TILE_256x256) return launch_cfg<256, 256, 2, 4, 64, 2, OUT, false, GROUPED, ACT_NONE, false, KM>(p, s);
@@ -51,7 +52,7 @@ static hipError_t launch_km(int tile, const gemm_params_t<OUT, GROUPED, KM>& p, 
 
 hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s) {
   constexpr int KM = 3 | kKmajorRagged;
-  if (p.kmajor != KM || p.groups < 1 || p.work_off == nullptr) return hipErrorInvalidValue;
+  if (p.kmajor != KM || p.groups < 1 || p.groups > kMaxGroups) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16 && p.ksplit <= 1 && p.act == ACT_NONE && p.bias == nullptr)
     return launch_km<GEMM_OUT_BF16, KM>(tile, p, s);
   if (out_kind == GEMM_OUT_F32_SCALED && p.row_scale == nullptr) return launch_km<GEMM_OUT_F32_SCALED, KM>(tile, p, s);
@@ -63,11 +64,13 @@ hipError_t launch_gemm_kmajor(int out_kind, int tile, const GemmTrainParams& p, 
   if ((p.kmajor & kSplitB) && (p.kb_split <= 0 || p.K != 2 * p.kb_split || p.kb_rows < 1 || p.kb_rows > p.kb_split))
     return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16 && p.ksplit <= 1) {
+    if (p.kmajor == 0) return launch_km<GEMM_OUT_BF16, 0>(tile, p, s);
     if (p.kmajor == (2 | kSplitB)) return launch_km<GEMM_OUT_BF16, 2 | kSplitB>(tile, p, s);
     if (p.kmajor == 3) return launch_km<GEMM_OUT_BF16, 3>(tile, p, s);
     if (p.kmajor == (3 | kSplitC) && p.C2 != nullptr) return launch_km<GEMM_OUT_BF16, 3 | kSplitC>(tile, p, s);
   }
   if (out_kind == GEMM_OUT_F32_SCALED) {
+    if (p.kmajor == 0) return launch_km<GEMM_OUT_F32_SCALED, 0>(tile, p, s);
     if (p.kmajor == (2 | kSplitB)) return launch_km<GEMM_OUT_F32_SCALED, 2 | kSplitB>(tile, p, s);
     if (p.kmajor == 3) return launch_km<GEMM_OUT_F32_SCALED, 3>(tile, p, s);
   }
@@ -81,7 +84,7 @@ hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hi
   if (out_kind == GEMM_OUT_GLU_SAVE && p.kmajor == 0)
     return by_act(p.act, [&](auto a) {
       return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s)
-                 : launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s);
+                 : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s);
     });
   if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 2)
     return by_act(p.act, [&](auto a) {
@@ -90,7 +93,7 @@ hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hi
     });
   if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 0 && !big)   // weights past the k-major span, transposed
     return by_act(p.act, [&](auto a) {
-      return launch_cfg<128, 128, 2, 2, 32, 4, GEMM_OUT_DGLU_SAVED, false, false, a.value>(p, s);
+      return launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value>(p, s);
     });
   return hipErrorInvalidValue;
 }

@@ -9,30 +9,11 @@ using namespace fmlp;
 
 namespace {
 
-constexpr int kMaxGroups = 1024;
 constexpr int64_t kMaxSpan = int64_t(1) << 30;   // elements of an operand read k-major: 2^31 bytes
 
 fmlp_status check_groups(int32_t E) {
   if (E < 1 || E > kMaxGroups) return fail(FMLP_E_ARG, "E=%d must be in [1, %d]", E, kMaxGroups);
   return FMLP_OK;
-}
-
-struct PlanLayout {
-  size_t group_off, tile_off, work_off, end;
-};
-PlanLayout plan_layout(int32_t E) {
-  PlanLayout L;
-  size_t o = kHeader;   // the decode header stays untouched
-  L.group_off = o; o += round_up(((size_t)E + 1) * 4, 256);
-  L.tile_off = o;  o += round_up(((size_t)E + 1) * 4, 256);
-  L.work_off = o;  o += round_up(((size_t)E + 1) * 8, 256);
-  L.end = o;
-  return L;
-}
-GroupPlan plan_at(void* workspace, const PlanLayout& L) {
-  char* ws = static_cast<char*>(workspace);
-  return {reinterpret_cast<int32_t*>(ws + L.group_off), reinterpret_cast<int32_t*>(ws + L.tile_off),
-          reinterpret_cast<int64_t*>(ws + L.work_off)};
 }
 
 GemmTrainParams train_params(const GemmParams& p) {
@@ -43,15 +24,25 @@ GemmTrainParams train_params(const GemmParams& p) {
 }
 
 // ---- tile and split of a product ------------------------------------------------
-// A product runs in rounds of one 256x256 tile per compute unit or two 128x128
-// ones, for as many 64-k stages as its longest tile has; splitting k in P parts
-// makes more, shorter tiles, and costs the parts' fp32 round trip and a launch.
-// The estimate of a candidate, in us, from times measured on the k-major forms
-// (a stage of a round, and what a tile costs beside its stages):
-constexpr double kStage256 = 1.50, kTile256 = 10.0;
-constexpr double kStage128 = 0.95, kTile128 = 6.0;
-constexpr double kPartsLaunch = 5.0, kPartsBytesPerUs = 4.0e6;
-constexpr int kPlanCus = 256;   // not the device's: workspaces are sized without one
+// A product runs in rounds of one 256x256 tile per compute unit (of 256: the
+// workspace is sized without a device) or two 128x128 ones, for as many 64-k
+// stages as a tile has; splitting k in P parts makes more, shorter tiles, and
+// costs the parts' fp32 round trip and a launch.  The estimate of a candidate in
+// us, fitted to the k-major forms over ten shapes from 256x256x8192 to
+// 14336x4096x4096 (2047x2048x11264: 98 us as 256 tiles in 4 parts, estimate 106;
+// 201 unsplit, 106 as 128 tiles in 2 parts; 4112x768x1001: 17 us as 128 tiles,
+// 29 as 256 tiles):
+constexpr double kPartsLaunch = 5.0, kPartsBytesPerUs = 5.0e6;
+// full rounds of 256 tiles, and a last one that runs faster the emptier it is
+double rounds256(int64_t tiles, int64_t stages) {
+  const int64_t full = tiles / 256, rest = tiles % 256;
+  return (double)full * (1.45 * (double)stages + 10) + (rest ? (1.10 + 0.35 * (double)rest / 256) * (double)stages + 8 : 0);
+}
+// full rounds of 512 tiles, two to a compute unit; up to 256 have one each
+double rounds128(int64_t tiles, int64_t stages) {
+  const int64_t full = tiles / 512, rest = tiles % 512;
+  return (double)full * ((double)stages + 4) + (rest == 0 ? 0 : (rest <= 256 ? 0.62 : 1.0) * (double)stages + 4);
+}
 
 struct ProductPlan {
   int tile, split;
@@ -65,10 +56,8 @@ ProductPlan plan_product(int64_t tiles256, int64_t tiles128, int64_t stages, int
     if (P > 1 && stages / P < 4) break;
     const double parts = P > 1 ? kPartsLaunch + 8.0 * P * (double)out / kPartsBytesPerUs : 0;
     for (int tile : {TILE_256x256, TILE_128x128}) {
-      const bool big = tile == TILE_256x256;
-      const int64_t rounds = ((big ? tiles256 : tiles128) * P + (big ? 1 : 2) * kPlanCus - 1) / ((big ? 1 : 2) * kPlanCus);
-      const double t = (double)rounds * ((double)((stages + P - 1) / P) * (big ? kStage256 : kStage128) +
-                                         (big ? kTile256 : kTile128)) + parts;
+      const int64_t st = (stages + P - 1) / P;
+      const double t = (tile == TILE_256x256 ? rounds256(tiles256 * P, st) : rounds128(tiles128 * P, st)) + parts;
       if (least == 0 || t < least) {
         least = t;
         best = {tile, P};
@@ -86,6 +75,29 @@ size_t parts_bytes(const ProductPlan& p, int64_t out) {
   return p.split > 1 ? round_up((size_t)p.split * (size_t)out * 4, 256) : 0;
 }
 
+// A product on its plan: C = A . B with the operands of `kmajor`; with C2, rows
+// [0, rows) of it are C's and rows [at, at + rows) C2's.
+hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, uint16_t* C2, int64_t at, int64_t rows,
+                       float* parts, hipStream_t s) {
+  if (plan.split == 1) {
+    p.C = C;
+    if (C2) {
+      p.C2 = C2;
+      p.c_split = at;
+      p.c_rows = rows;
+      p.kmajor |= kSplitC;
+    }
+    return launch_gemm_kmajor(GEMM_OUT_BF16, plan.tile, p, s);
+  }
+  p.C = parts;
+  p.ksplit = plan.split;
+  p.c_kstride = p.M * p.N;
+  hipError_t e = launch_gemm_kmajor(GEMM_OUT_F32_SCALED, plan.tile, p, s);
+  if (e == hipSuccess) e = launch_sum_parts(parts, plan.split, p.M * p.N, (C2 ? rows : p.M) * p.N, C, s);
+  if (e == hipSuccess && C2) e = launch_sum_parts(parts + at * p.N, plan.split, p.M * p.N, rows * p.N, C2, s);
+  return e;
+}
+
 // The row tiles of E ragged groups: the sizes are on the device, so the mean
 // R / E stands for them, with half a tile wasted per group.
 bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
@@ -93,11 +105,11 @@ bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
   return plan_product(t256, t128, (K + 63) / 64, R * N, 1).tile == TILE_256x256;
 }
 
-void set_groups(GemmTrainParams& p, const GroupPlan& plan, int32_t E, int64_t R, bool big) {
+void set_groups(GemmTrainParams& p, const int32_t* group_off, int32_t E, int64_t R, bool big) {
   const int bm = big ? 256 : 128;
-  p.group_off = plan.group_off;
-  p.tile_off = plan.tile_off;
+  p.group_off = group_off;
   p.groups = E;
+  p.group_rows = R;
   p.tiles_m = (int)(R / bm + E);   // at most one partial tile per group
 }
 
@@ -107,15 +119,13 @@ ProductPlan plan_grouped_dw(int64_t R, int64_t N, int64_t K, int32_t E) {
 }
 
 struct GroupedBwdLayout {
-  PlanLayout plan;
   size_t dz, parts, total;
   ProductPlan dw;
 };
 GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, int act) {
   GroupedBwdLayout L;
-  L.plan = plan_layout(E);
   L.dw = plan_grouped_dw(R, N, K, E);
-  size_t o = L.plan.end;
+  size_t o = kHeader;   // the decode header stays untouched
   L.dz = o;    o += act != FMLP_ACT_NONE ? ws_bf16(R, N) : 0;
   L.parts = o; o += parts_bytes(L.dw, E * N * K);
   L.total = o;
@@ -126,13 +136,8 @@ GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, 
 
 extern "C" {
 
-size_t fmlp_grouped_linear_workspace_size(int32_t E) {
-  return E < 1 || E > kMaxGroups ? 0 : plan_layout(E).end;
-}
-
 fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W, const fmlp_bf16* b,
-                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, void* workspace,
-                                size_t workspace_bytes, fmlp_stream stream) {
+                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, fmlp_stream stream) {
   TRY(check_rows("R", R));
   TRY(check_inner("K", K));
   TRY(check_inner("N", N));
@@ -143,17 +148,13 @@ fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, co
   REQUIRE_PTR(W);
   OPTIONAL_PTR(b);
   TOKEN_PTR(y, R);
-  const PlanLayout L = plan_layout(E);
-  TRY(check_workspace(workspace, workspace_bytes, L.end));
   if (R == 0) return ok();
   int cus = 0;
   TRY(check_device(&cus));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const GroupPlan plan = plan_at(workspace, L);
   const bool big = grouped_big(R, N, K, E);
-  HIP_TRY(launch_group_plan(group_off, R, E, big ? 256 : 128, 1, plan, s), "grouped_linear plan launch");
   GemmTrainParams p = train_params(dense_params(x, K, W, nullptr, b, y, N, R, N, K, act, cus));
-  set_groups(p, plan, E, R, big);
+  set_groups(p, group_off, E, R, big);
   p.strideB = N * K;
   p.stride_bias = N;
   return launched(launch_gemm_grouped(GEMM_OUT_BF16, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear launch");
@@ -196,30 +197,27 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
     return ok();
   }
   char* ws = static_cast<char*>(workspace);
-  const GroupPlan plan = plan_at(workspace, L.plan);
-  // one plan serves dz and dx: both run on row tiles of the same height
-  const bool big = grouped_big(R, K, N, E);
-  const int tile = big ? TILE_256x256 : TILE_128x128;
-  HIP_TRY(launch_group_plan(group_off, R, E, big ? 256 : 128, L.dw.split, plan, s), "grouped_linear_bwd plan launch");
   const uint16_t* dz = dy;
   if (act != FMLP_ACT_NONE) {   // dz = dy * act'(x W^T + b), z recomputed
     uint16_t* dzw = reinterpret_cast<uint16_t*>(ws + L.dz);
+    const bool big = grouped_big(R, N, K, E);
     GemmTrainParams p = train_params(dense_params(x, K, W, nullptr, b, dzw, N, R, N, K, act, cus));
-    set_groups(p, plan, E, R, big);
+    set_groups(p, group_off, E, R, big);
     p.strideB = N * K;
     p.stride_bias = N;
     p.E = dy;
     p.lde = N;
-    HIP_TRY(launch_gemm_grouped(GEMM_OUT_DACT, tile, p, s), "grouped_linear_bwd dz launch");
+    HIP_TRY(launch_gemm_grouped(GEMM_OUT_DACT, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dz launch");
     dz = dzw;
   }
   {   // dx = dz W[e]: the contraction runs over W's rows, read k-major
+    const bool big = grouped_big(R, K, N, E);
     GemmTrainParams p = train_params(dense_params(dz, N, W, nullptr, nullptr, dx, K, R, K, N, FMLP_ACT_NONE, cus));
-    set_groups(p, plan, E, R, big);
+    set_groups(p, group_off, E, R, big);
     p.strideB = N * K;
     p.kmajor = 2;
     p.ldb = K;
-    HIP_TRY(launch_gemm_grouped(GEMM_OUT_BF16, tile, p, s), "grouped_linear_bwd dx launch");
+    HIP_TRY(launch_gemm_grouped(GEMM_OUT_BF16, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dx launch");
   }
   {   // dW[e] = dz^T x over the group's rows, both read k-major
     float* parts = reinterpret_cast<float*>(ws + L.parts);
@@ -228,9 +226,9 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
                                                   K, R, FMLP_ACT_NONE, cus));
     p.kmajor = 3 | kKmajorRagged;
     p.ldb = K;
-    p.group_off = plan.group_off;
-    p.work_off = plan.work_off;
+    p.group_off = group_off;
     p.groups = E;
+    p.group_rows = R;
     p.stride_c = N * K;
     if (split) {
       p.ksplit = L.dw.split;
@@ -239,7 +237,7 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
     HIP_TRY(launch_gemm_ragged(split ? GEMM_OUT_F32_SCALED : GEMM_OUT_BF16, L.dw.tile, p, s), "grouped_linear_bwd dW launch");
     if (split) HIP_TRY(launch_sum_parts(parts, L.dw.split, E * N * K, E * N * K, dW, s), "grouped_linear_bwd dW sum");
   }
-  if (db) HIP_TRY(launch_group_colsum(dz, plan.group_off, E, N, db, s), "grouped_linear_bwd db launch");
+  if (db) HIP_TRY(launch_group_colsum(dz, group_off, R, E, N, db, s), "grouped_linear_bwd db launch");
   return ok();
 }
 
@@ -248,7 +246,7 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
 // ---------------------------------------------------------------------------
 size_t fmlp_glu_ckpt_workspace_size(int64_t M, int64_t D, int64_t H) {
   if (M < 0 || D <= 0 || H <= 0) return 0;
-  return kHeader + ws_bf16(M, H);
+  return kHeader + ws_bf16(M, H) + parts_bytes(plan_dense(M, D, H), M * D);
 }
 
 size_t fmlp_glu_ckpt_codes_size(int64_t M, int64_t H) { return M < 0 || H <= 0 ? 0 : (size_t)M * (size_t)H * 2; }
@@ -280,8 +278,10 @@ fmlp_status fmlp_glu_ckpt(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf
   GemmTrainParams p = train_params(dense_params(x, D, Wg, Wu, nullptr, m, H, M, H, D, gate_act, cus));
   p.codes = codes;
   p.qscale = scales;
-  HIP_TRY(launch_gemm_ckpt(GEMM_OUT_GLU_SAVE, choose_tile(M, (H + 127) / 128, cus), p, s), "glu_ckpt gate+up launch");
-  return launched(gemm_linear(m, Wd, nullptr, FMLP_ACT_NONE, M, H, D, y, cus, s), "glu_ckpt down launch");
+  HIP_TRY(launch_gemm_ckpt(GEMM_OUT_GLU_SAVE, plan_dense(M, 2 * H, D, 1).tile, p, s), "glu_ckpt gate+up launch");
+  p = train_params(dense_params(m, H, Wd, nullptr, nullptr, nullptr, D, M, D, H, FMLP_ACT_NONE, cus));
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader + ws_bf16(M, H));
+  return launched(run_product(plan_dense(M, D, H), p, y, nullptr, 0, 0, parts, s), "glu_ckpt down launch");
 }
 
 namespace {
@@ -314,28 +314,6 @@ CkptBwdLayout ckpt_bwd_layout(int64_t M, int64_t D, int64_t H) {
                 : std::max(ws_bf16(H, D), glu_products_scratch(M, D, H));
   L.total = o;
   return L;
-}
-// A product on its plan: C = A . B with the operands of `kmajor`; with C2, rows
-// [0, rows) of it are C's and rows [at, at + rows) C2's.
-hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, uint16_t* C2, int64_t at, int64_t rows,
-                       float* parts, hipStream_t s) {
-  if (plan.split == 1) {
-    p.C = C;
-    if (C2) {
-      p.C2 = C2;
-      p.c_split = at;
-      p.c_rows = rows;
-      p.kmajor |= kSplitC;
-    }
-    return launch_gemm_kmajor(GEMM_OUT_BF16, plan.tile, p, s);
-  }
-  p.C = parts;
-  p.ksplit = plan.split;
-  p.c_kstride = p.M * p.N;
-  hipError_t e = launch_gemm_kmajor(GEMM_OUT_F32_SCALED, plan.tile, p, s);
-  if (e == hipSuccess) e = launch_sum_parts(parts, plan.split, p.M * p.N, (C2 ? rows : p.M) * p.N, C, s);
-  if (e == hipSuccess && C2) e = launch_sum_parts(parts + at * p.N, plan.split, p.M * p.N, rows * p.N, C2, s);
-  return e;
 }
 }  // namespace
 

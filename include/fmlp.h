@@ -236,8 +236,9 @@ size_t fmlp_glu_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
  * u are scaled by that power of two from the fp32 accumulators, which rounds
  * nothing, and rounded once to E4M3 (nearest, ties to even): by at most 2^-4 of
  * a value down to 2^-6 in the scaled unit, and 2^-10 in that unit below.  An
- * infinity or a NaN does not enter the scale and is stored as NaN.  y is that
- * of fmlp_glu's two-launch path: it does not see the 8 bits.
+ * infinity or a NaN does not enter the scale and is stored as NaN.  y is
+ * fmlp_glu's and does not see the 8 bits (where its product is split over H, the
+ * parts are added in fp32 in a fixed order, so the last bit may differ).
  *
  * The gradients are those of fmlp_glu_bwd's formulas at the stored g and u:
  *   m = act(g) * u, dWd = dy^T m, dm = dy Wd, dg = dm * u * act'(g),
@@ -289,12 +290,11 @@ size_t fmlp_glu_ckpt_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
  * group are left as they were.  R K, R N and N K must each be below 2^30
  * (FMLP_E_SHAPE).  Both operands of dW and the weights of dx are read as
  * stored.  Bitwise deterministic.
- * Workspaces need no initialisation and leave the first 8192 bytes alone.
+ * The forward is one launch without a workspace; the backward's needs no
+ * initialisation, and its first 8192 bytes are left alone.
  */
 fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W, const fmlp_bf16* b,
-                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, void* workspace,
-                                size_t workspace_bytes, fmlp_stream stream);
-size_t fmlp_grouped_linear_workspace_size(int32_t E);
+                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, fmlp_stream stream);
 fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W,
                                     const fmlp_bf16* b, int act, const fmlp_bf16* dy, int64_t R, int64_t K, int64_t N,
                                     int32_t E, fmlp_bf16* dx, fmlp_bf16* dW, fmlp_bf16* db, void* workspace,

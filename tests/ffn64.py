@@ -115,6 +115,14 @@ def grouped_bwd(x, off, W, b, act, dy):
     return (dx, dW, db), (edx, edW, edb)
 
 
+def glu(x, Wg, Wu, Wd, act):
+    """The gated block and its bound"""
+    (g, eg), (u, eu) = mm(x, Wg.t()), mm(x, Wu.t())
+    m, em = prod(act64(g, act)[0], act_err(g, eg, act)[0], u, eu)
+    y, e = mm(m, Wd.t(), rounded(m, em))
+    return y, rounded(y, e)
+
+
 def glu_bwd_at(g, u, x, Wg, Wu, Wd, act, dy):
     """The gated block's gradients at given g and u, and their bounds"""
     z = torch.zeros_like(g)

@@ -277,7 +277,8 @@ def test_refusals():
                       (lambda: F.fmlp_grouped_linear(x, offs, W, b[0]), ValueError),
                       (lambda: F.fmlp_grouped_linear(x, offs, W, out=dy[:4]), ValueError),
                       (lambda: F.fmlp_grouped_linear(x, offs, W, b, "tanh"), KeyError),
-                      (lambda: F.fmlp_grouped_linear(x, offs, W, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), F.FmlpError),
+                      (lambda: F.fmlp_grouped_linear_bwd(x, offs, W, b, "silu", dy,
+                                                         workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), F.FmlpError),
                       (lambda: F.fmlp_grouped_linear_bwd(x, offs, W, b, "none", dy[:4]), ValueError),
                       (lambda: F.fmlp_grouped_linear_bwd(x, offs, W, b, "none", dy.float()), TypeError)):
         with pytest.raises(err):
