@@ -132,6 +132,8 @@ _sz = ctypes.c_size_t
 def lib() -> ctypes.CDLL:
     """Load libfmlp.so (built in-tree).  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is not None:
             return _lib
@@ -512,38 +514,79 @@ def bind_glu_bwd(x, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None) -> 
 # ---------------------------------------------------------------------------
 # products grouped by expert; the gated block with an 8-bit checkpoint
 # ---------------------------------------------------------------------------
-def _scratch(like: torch.Tensor, workspace, nbytes: int) -> torch.Tensor:
-    """The caller's workspace, or fresh memory of the current stream's pool: these calls need no initialised
-    header, and memory of a call's own is safe for captured graphs that replay on different streams."""
-    if workspace is not None:
-        if workspace.dtype != torch.uint8:
-            raise TypeError(f"workspace must be torch.uint8 (got {workspace.dtype})")
-        _same_device(like, workspace=workspace)
-        return _dev_tensor("workspace", workspace, torch.uint8)
-    return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+# The calls below check and marshal on the shortest path that still names what is
+# wrong: at a few microseconds a kernel, the binding is most of a small call.
+def _need(name: str, t, dtype, device: int) -> None:
+    """t is a contiguous tensor of dtype on GPU `device` (the index of x's)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        _dev_tensor(name, t, dtype)   # raises with the reason
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, x on cuda:{device}")
 
 
-def _same_device(like: torch.Tensor, **tensors) -> None:
-    for n, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{n} is on {t.device}, x on {like.device}")
+def _need_x(x) -> int:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        _dev_tensor("x", x)
+    device = x.get_device()
+    _need("x", x, torch.bfloat16, device)
+    return device
 
 
-def _out(name, t, shape, like, dtype=torch.bfloat16) -> torch.Tensor:
+def _scratch(device: int, workspace, nbytes: int):
+    """(memory, its address, its size): the caller's workspace, or fresh memory of the current stream's pool.  These
+    calls need no initialised header, and memory of a call's own is safe for captured graphs that replay on
+    different streams."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        _need("workspace", workspace, torch.uint8, device)
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _out(name, t, shape, device: int, dtype=torch.bfloat16) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _dev_tensor(name, t, dtype)
-    _same_device(like, **{name: t})
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(name, t, dtype, device)
     if t.shape != torch.Size(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
-def _grouped_args(x, group_off, W, b):
-    _dev_tensor("x", x)
-    _dev_tensor("W", W)
-    _dev_tensor("group_off", group_off, torch.int32)
-    _same_device(x, W=W, group_off=group_off, b=b)
+def _on(device: int, marshal, *args):
+    """(function, arguments, result, tensors to keep) of a call, marshalled with x's device current."""
+    if device == torch.cuda.current_device():
+        return marshal(device, *args)
+    with torch.cuda.device(device):
+        return marshal(device, *args)
+
+
+def _call(x, marshal, *args):
+    device = _need_x(x)
+    if device == torch.cuda.current_device():
+        fn, a, out, _ = marshal(device, x, *args)
+        st = fn(*a)
+    else:
+        with torch.cuda.device(device):
+            fn, a, out, _ = marshal(device, x, *args)
+            st = fn(*a)
+    if st:
+        _check(st)
+    return out
+
+
+def _bind(x, marshal, *args) -> BoundCall:
+    return BoundCall(*_on(_need_x(x), marshal, x, *args))
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _grouped_args(device, x, group_off, W, b):
+    _need("W", W, torch.bfloat16, device)
+    _need("group_off", group_off, torch.int32, device)
     if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
         raise ValueError(f"x must be [R, K] and W [E, N, K], got {tuple(x.shape)} and {tuple(W.shape)}")
     R, K = x.shape
@@ -551,17 +594,17 @@ def _grouped_args(x, group_off, W, b):
     if group_off.shape != (E + 1,):
         raise ValueError(f"group_off must be [{E + 1}] int32, got {tuple(group_off.shape)}")
     if b is not None:
-        _dev_tensor("b", b)
+        _need("b", b, torch.bfloat16, device)
         if b.shape != (E, N):
             raise ValueError(f"b must be [{E}, {N}], got {tuple(b.shape)}")
     return R, K, N, E
 
 
-def _grouped_linear_call(x, group_off, W, b, act, out):
-    R, K, N, E = _grouped_args(x, group_off, W, b)
-    y = _out("out", out, (R, N), x)
-    return BoundCall(lib().fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K,
-                                                 N, E, y.data_ptr(), _stream(x.device)), y, (x, group_off, W, b))
+def _grouped_linear_call(device, x, group_off, W, b, act, out):
+    R, K, N, E = _grouped_args(device, x, group_off, W, b)
+    y = _out("out", out, (R, N), device)
+    return (lib().fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K, N, E,
+                                        y.data_ptr(), _raw_stream(device)), y, (x, group_off, W, b))
 
 
 def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None):
@@ -569,67 +612,60 @@ def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None):
 
     x [R, K]; group_off int32 [E + 1] on the device; W [E, N, K]; b [E, N] or None -> y [R, N].  Rows outside every
     group are not written: with out=None they hold whatever the new tensor held."""
-    with torch.cuda.device(x.device):
-        return _grouped_linear_call(x, group_off, W, b, act, out)()
+    return _call(x, _grouped_linear_call, group_off, W, b, act, out)
 
 
 def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _grouped_linear_call(x, group_off, W, b, act, out)
+    return _bind(x, _grouped_linear_call, group_off, W, b, act, out)
 
 
-def _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace):
-    R, K, N, E = _grouped_args(x, group_off, W, b)
-    _dev_tensor("dy", dy)
-    _same_device(x, dy=dy)
+def _grouped_linear_bwd_call(device, x, group_off, W, b, act, dy, out, workspace):
+    R, K, N, E = _grouped_args(device, x, group_off, W, b)
+    _need("dy", dy, torch.bfloat16, device)
     if dy.shape != (R, N):
         raise ValueError(f"dy must be [{R}, {N}], got {tuple(dy.shape)}")
     dx, dW, db = out if out is not None else (None, None, None)
-    dx = _out("dx", dx, (R, K), x)
-    dW = _out("dW", dW, (E, N, K), x)
+    dx = _out("dx", dx, (R, K), device)
+    dW = _out("dW", dW, (E, N, K), device)
     if b is not None or db is not None:
-        db = _out("db", db, (E, N), x)
+        db = _out("db", db, (E, N), device)
     L = lib()
-    ws = _scratch(x, workspace, L.fmlp_grouped_linear_bwd_workspace_size(R, K, N, E, ACT[act]))
-    return BoundCall(L.fmlp_grouped_linear_bwd, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act],
-                                                 dy.data_ptr(), R, K, N, E, dx.data_ptr(), dW.data_ptr(), _ptr(db),
-                                                 ws.data_ptr(), ws.numel(), _stream(x.device)),
-                     (dx, dW, db), (x, group_off, W, b, dy, ws))
+    ws, wp, wn = _scratch(device, workspace, L.fmlp_grouped_linear_bwd_workspace_size(R, K, N, E, ACT[act]))
+    return (L.fmlp_grouped_linear_bwd, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], dy.data_ptr(),
+                                        R, K, N, E, dx.data_ptr(), dW.data_ptr(), _ptr(db), wp, wn, _raw_stream(device)),
+            (dx, dW, db), (x, group_off, W, b, dy, ws))
 
 
 def fmlp_grouped_linear_bwd(x, group_off, W, b, act: str, dy, out=None, workspace=None):
     """Gradients of fmlp_grouped_linear: returns (dx [R, K], dW [E, N, K], db [E, N], or None without b).  Rows of dx
     outside every group are not written."""
-    with torch.cuda.device(x.device):
-        return _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace)()
+    return _call(x, _grouped_linear_bwd_call, group_off, W, b, act, dy, out, workspace)
 
 
 def bind_grouped_linear_bwd(x, group_off, W, b, act: str, dy, out=None, workspace=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _grouped_linear_bwd_call(x, group_off, W, b, act, dy, out, workspace)
+    return _bind(x, _grouped_linear_bwd_call, group_off, W, b, act, dy, out, workspace)
 
 
-def _ckpt_args(x, Wg, Wu, Wd):
-    for n, t in (("x", x), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd)):
-        _dev_tensor(n, t)
-    _same_device(x, Wg=Wg, Wu=Wu, Wd=Wd)
+def _ckpt_args(device, x, Wg, Wu, Wd):
+    for n, t in (("Wg", Wg), ("Wu", Wu), ("Wd", Wd)):
+        _need(n, t, torch.bfloat16, device)
     D, H = x.shape[-1], Wg.shape[0]
     if Wg.shape != (H, D) or Wu.shape != (H, D) or Wd.shape != (D, H):
         raise ValueError(f"shape mismatch: x[...,{D}] Wg{tuple(Wg.shape)} Wu{tuple(Wu.shape)} Wd{tuple(Wd.shape)}")
     return x.numel() // D, D, H
 
 
-def _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace):
-    M, D, H = _ckpt_args(x, Wg, Wu, Wd)
+def _glu_ckpt_call(device, x, Wg, Wu, Wd, gate_act, out, workspace):
+    M, D, H = _ckpt_args(device, x, Wg, Wu, Wd)
     y, codes, scales = out if out is not None else (None, None, None)
-    y = _out("y", y, x.shape, x)
-    codes = _out("codes", codes, (M, 2 * H), x, torch.uint8)
-    scales = _out("scales", scales, (M, 2 * ((H + 31) // 32)), x, torch.uint8)
+    y = _out("y", y, x.shape, device)
+    codes = _out("codes", codes, (M, 2 * H), device, torch.uint8)
+    scales = _out("scales", scales, (M, 2 * ((H + 31) // 32)), device, torch.uint8)
     L = lib()
-    ws = _scratch(x, workspace, L.fmlp_glu_ckpt_workspace_size(M, D, H))
-    return BoundCall(L.fmlp_glu_ckpt, (x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), ACT[gate_act], M, D, H,
-                                       y.data_ptr(), codes.data_ptr(), scales.data_ptr(), ws.data_ptr(), ws.numel(),
-                                       _stream(x.device)), (y, codes, scales), (x, Wg, Wu, Wd, ws))
+    ws, wp, wn = _scratch(device, workspace, L.fmlp_glu_ckpt_workspace_size(M, D, H))
+    return (L.fmlp_glu_ckpt, (x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), ACT[gate_act], M, D, H,
+                              y.data_ptr(), codes.data_ptr(), scales.data_ptr(), wp, wn, _raw_stream(device)),
+            (y, codes, scales), (x, Wg, Wu, Wd, ws))
 
 
 def fmlp_glu_ckpt(x, Wg, Wu, Wd, gate_act: str = "silu", out=None, workspace=None):
@@ -637,47 +673,42 @@ def fmlp_glu_ckpt(x, Wg, Wu, Wd, gate_act: str = "silu", out=None, workspace=Non
 
     codes uint8 [M, 2H] (E4M3, g then u), scales uint8 [M, 2 ceil(H / 32)]: value = e4m3(code) * 2**(scale - 127)
     for the scale of its row and block of 32 hidden units."""
-    with torch.cuda.device(x.device):
-        return _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace)()
+    return _call(x, _glu_ckpt_call, Wg, Wu, Wd, gate_act, out, workspace)
 
 
 def bind_glu_ckpt(x, Wg, Wu, Wd, gate_act: str = "silu", out=None, workspace=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _glu_ckpt_call(x, Wg, Wu, Wd, gate_act, out, workspace)
+    return _bind(x, _glu_ckpt_call, Wg, Wu, Wd, gate_act, out, workspace)
 
 
-def _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace):
-    M, D, H = _ckpt_args(x, Wg, Wu, Wd)
-    _dev_tensor("dy", dy)
+def _glu_ckpt_bwd_call(device, x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace):
+    M, D, H = _ckpt_args(device, x, Wg, Wu, Wd)
+    _need("dy", dy, torch.bfloat16, device)
     codes = _w8_codes("codes", codes)
-    _dev_tensor("scales", scales, torch.uint8)
-    _same_device(x, dy=dy, codes=codes, scales=scales)
+    _need("codes", codes, torch.uint8, device)
+    _need("scales", scales, torch.uint8, device)
     if dy.shape != x.shape:
         raise ValueError(f"dy must be {tuple(x.shape)}, got {tuple(dy.shape)}")
     if codes.shape != (M, 2 * H) or scales.shape != (M, 2 * ((H + 31) // 32)):
         raise ValueError(f"codes must be [{M}, {2 * H}] and scales [{M}, {2 * ((H + 31) // 32)}], got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     dx, dWg, dWu, dWd = out if out is not None else (None, None, None, None)
-    dx, dWg, dWu, dWd = (_out(n, t, s, x) for n, t, s in (("dx", dx, x.shape), ("dWg", dWg, (H, D)),
-                                                          ("dWu", dWu, (H, D)), ("dWd", dWd, (D, H))))
+    dx, dWg, dWu, dWd = (_out(n, t, s, device) for n, t, s in (("dx", dx, x.shape), ("dWg", dWg, (H, D)),
+                                                               ("dWu", dWu, (H, D)), ("dWd", dWd, (D, H))))
     L = lib()
-    ws = _scratch(x, workspace, L.fmlp_glu_ckpt_bwd_workspace_size(M, D, H))
-    return BoundCall(L.fmlp_glu_ckpt_bwd, (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), Wg.data_ptr(),
-                                           Wu.data_ptr(), Wd.data_ptr(), ACT[gate_act], dy.data_ptr(), M, D, H,
-                                           dx.data_ptr(), dWg.data_ptr(), dWu.data_ptr(), dWd.data_ptr(), ws.data_ptr(),
-                                           ws.numel(), _stream(x.device)),
-                     (dx, dWg, dWu, dWd), (x, codes, scales, Wg, Wu, Wd, dy, ws))
+    ws, wp, wn = _scratch(device, workspace, L.fmlp_glu_ckpt_bwd_workspace_size(M, D, H))
+    return (L.fmlp_glu_ckpt_bwd, (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+                                  Wd.data_ptr(), ACT[gate_act], dy.data_ptr(), M, D, H, dx.data_ptr(), dWg.data_ptr(),
+                                  dWu.data_ptr(), dWd.data_ptr(), wp, wn, _raw_stream(device)),
+            (dx, dWg, dWu, dWd), (x, codes, scales, Wg, Wu, Wd, dy, ws))
 
 
 def fmlp_glu_ckpt_bwd(x, codes, scales, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None):
     """Gradients of the gated block at the g and u that fmlp_glu_ckpt kept: returns (dx, dWg, dWu, dWd)."""
-    with torch.cuda.device(x.device):
-        return _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)()
+    return _call(x, _glu_ckpt_bwd_call, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)
 
 
 def bind_glu_ckpt_bwd(x, codes, scales, Wg, Wu, Wd, gate_act: str, dy, out=None, workspace=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _glu_ckpt_bwd_call(x, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)
+    return _bind(x, _glu_ckpt_bwd_call, codes, scales, Wg, Wu, Wd, gate_act, dy, out, workspace)
 
 
 def fmlp_moe_workspace_size(T, D, H, E, top_k) -> int:
@@ -911,77 +942,66 @@ def bind_glu_w8(x, Wgq, sg, Wuq, su, Wdq, sd, gate_act: str = "gelu_tanh", out=N
 # ---------------------------------------------------------------------------
 # 4-bit weights with group scales, decode
 # ---------------------------------------------------------------------------
-def _w4_weight(name, q, s, z, N, K, x) -> int:
+def _w4_weight(name, q, s, z, N, K, device) -> int:
     """Checks one 4-bit weight [N, K] and returns its group size."""
-    _dev_tensor(name, q, torch.uint8)
-    _dev_tensor(f"{name}'s scales", s)
-    _same_device(x, **{name: q, f"{name}'s scales": s})
-    if q.shape != (N, K // 2) or K % 2:
+    _need(name, q, torch.uint8, device)
+    _need(f"{name}'s scales", s, torch.bfloat16, device)
+    if K % 2 or q.shape != (N, K // 2):
         raise ValueError(f"{name} must be [{N}, {K // 2}] (two codes a byte), got {tuple(q.shape)}")
-    if s.dim() != 2 or s.shape[0] != N or s.shape[1] == 0 or K % s.shape[1]:
-        raise ValueError(f"{name}'s scales must be [{N}, {K} / group], got {tuple(s.shape)}")
+    shape = s.shape
+    if len(shape) != 2 or shape[0] != N or shape[1] == 0 or K % shape[1]:
+        raise ValueError(f"{name}'s scales must be [{N}, {K} / group], got {tuple(shape)}")
     if z is not None:
-        _dev_tensor(f"{name}'s zeros", z)
-        _same_device(x, **{f"{name}'s zeros": z})
-        if z.shape != s.shape:
-            raise ValueError(f"{name}'s zeros must be {tuple(s.shape)}, got {tuple(z.shape)}")
-    return K // s.shape[1]
+        _need(f"{name}'s zeros", z, torch.bfloat16, device)
+        if z.shape != shape:
+            raise ValueError(f"{name}'s zeros must be {tuple(shape)}, got {tuple(z.shape)}")
+    return K // shape[1]
 
 
-def _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace):
-    _dev_tensor("x", x)
+def _linear_w4_call(device, x, Wq, scales, zeros, b, act, out, workspace):
     K, N = x.shape[-1], Wq.shape[0]
-    G = _w4_weight("Wq", Wq, scales, zeros, N, K, x)
+    G = _w4_weight("Wq", Wq, scales, zeros, N, K, device)
     if b is not None:
-        _dev_tensor("b", b)
-        _same_device(x, b=b)
+        _need("b", b, torch.bfloat16, device)
         if b.shape != (N,):
             raise ValueError(f"b must be [{N}], got {tuple(b.shape)}")
-    y = _out("out", out, x.shape[:-1] + (N,), x)
+    y = _out("out", out, x.shape[:-1] + (N,), device)
     L = lib()
     M = x.numel() // K
-    need = L.fmlp_linear_w4_workspace_size(M, K, N, G)
-    ws = _scratch(x, workspace, need) if need else None
-    return BoundCall(L.fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act],
-                                        M, K, N, G, y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-                                        _stream(x.device)), y, (x, Wq, scales, zeros, b, ws))
+    ws, wp, wn = _scratch(device, workspace, L.fmlp_linear_w4_workspace_size(M, K, N, G))
+    return (L.fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act], M, K, N, G,
+                               y.data_ptr(), wp, wn, _raw_stream(device)), y, (x, Wq, scales, zeros, b, ws))
 
 
 def fmlp_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None, workspace=None):
     """y = act(x W^T + b), W[n, k] = scales[n, k // G] * (code[n, k] - zeros[n, k // G]); x [..., K], at most 16 rows.
 
     Wq uint8 [N, K / 2], code 2j in the low half of byte j; scales (and zeros, or None for 8) bf16 [N, K / G]."""
-    with torch.cuda.device(x.device):
-        return _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace)()
+    return _call(x, _linear_w4_call, Wq, scales, zeros, b, act, out, workspace)
 
 
 def bind_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None, workspace=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _linear_w4_call(x, Wq, scales, zeros, b, act, out, workspace)
+    return _bind(x, _linear_w4_call, Wq, scales, zeros, b, act, out, workspace)
 
 
-def _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace):
-    _dev_tensor("x", x)
+def _glu_w4_call(device, x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace):
     D, H = x.shape[-1], Wgq.shape[0]
-    G = _w4_weight("Wgq", Wgq, sg, zg, H, D, x)
-    if _w4_weight("Wuq", Wuq, su, zu, H, D, x) != G or _w4_weight("Wdq", Wdq, sd, zd, D, H, x) != G:
+    G = _w4_weight("Wgq", Wgq, sg, zg, H, D, device)
+    if _w4_weight("Wuq", Wuq, su, zu, H, D, device) != G or _w4_weight("Wdq", Wdq, sd, zd, D, H, device) != G:
         raise ValueError("the three weights must have the same group size")
     M = x.numel() // D
-    y = _out("out", out, x.shape, x)
+    y = _out("out", out, x.shape, device)
     L = lib()
-    ws = _scratch(x, workspace, L.fmlp_glu_w4_workspace_size(M, D, H, G))
-    return BoundCall(L.fmlp_glu_w4, (x.data_ptr(), Wgq.data_ptr(), sg.data_ptr(), _ptr(zg), Wuq.data_ptr(), su.data_ptr(),
-                                     _ptr(zu), Wdq.data_ptr(), sd.data_ptr(), _ptr(zd), ACT[gate_act], M, D, H, G,
-                                     y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(x.device)), y,
-                     (x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, ws))
+    ws, wp, wn = _scratch(device, workspace, L.fmlp_glu_w4_workspace_size(M, D, H, G))
+    return (L.fmlp_glu_w4, (x.data_ptr(), Wgq.data_ptr(), sg.data_ptr(), _ptr(zg), Wuq.data_ptr(), su.data_ptr(), _ptr(zu),
+                            Wdq.data_ptr(), sd.data_ptr(), _ptr(zd), ACT[gate_act], M, D, H, G, y.data_ptr(), wp, wn,
+                            _raw_stream(device)), y, (x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, ws))
 
 
 def fmlp_glu_w4(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act: str = "silu", out=None, workspace=None):
     """fmlp_glu with 4-bit weights (Wgq, Wuq [H, D / 2], Wdq [D, H / 2], scales and zeros as for fmlp_linear_w4)."""
-    with torch.cuda.device(x.device):
-        return _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)()
+    return _call(x, _glu_w4_call, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)
 
 
 def bind_glu_w4(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act: str = "silu", out=None, workspace=None) -> BoundCall:
-    with torch.cuda.device(x.device):
-        return _glu_w4_call(x, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)
+    return _bind(x, _glu_w4_call, Wgq, sg, zg, Wuq, su, zu, Wdq, sd, zd, gate_act, out, workspace)

@@ -810,12 +810,48 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   };
   // The activation is a template argument so each copy of the epilogue is
   // straight-line code (a per-element switch would branch around every value).
+  // What an epilogue of the new forms reads beside the accumulator (dy, or the
+  // checkpoint's codes and exponents), for one activation fragment: requested a
+  // fragment ahead.  The accumulator reads are ordered after the stores before
+  // them, so a load left where it is used would wait out a round trip per run
+  // (44 us a 256x256 tile of the checkpoint's dm product, 14 us of them now).
+  struct Ahead {
+    u32x4_t v[RUNS];     // dy; or g's codes (words 0, 1) and u's (2, 3)
+    uint32_t e[RUNS];    // the exponents of g (low byte) and u
+  };
+  constexpr bool AHEAD = OUT == GEMM_OUT_DGLU_SAVED || (OUT == GEMM_OUT_DACT && TRAIN);
+  auto ahead = [&](const Tile& t, int i, int li, int lg, Ahead& a) {
+    if constexpr (AHEAD) {
+      const int64_t lrow = t.row_begin + wm * TM + i * MR + li;
+#pragma unroll
+      for (int q = 0; q < RUNS; ++q) {
+        const int64_t n = t.n0 + wn * TN + run_col(q, lg);
+        if (!(lrow < t.row_end && n < N)) continue;
+        if constexpr (OUT == GEMM_OUT_DACT) {
+          a.v[q] = gld16(p.E + lrow * p.lde + n);
+        } else {
+          const int64_t nb = (N + kCkptBlock - 1) / kCkptBlock;
+          const uint8_t* code = p.codes + lrow * 2 * N + n;
+          const uint8_t* sc = p.qscale + lrow * 2 * nb + n / kCkptBlock;
+          uint32_t c[4];
+          gld8(code, c);
+          gld8(code + N, c + 2);
+          a.v[q] = u32x4_t{c[0], c[1], c[2], c[3]};
+          a.e[q] = (uint32_t)*(const gu8_t*)sc | (uint32_t)*(const gu8_t*)(sc + nb) << 8;
+        }
+      }
+    }
+  };
   auto epilogue_act = [&](const Tile& t, auto act_c) {
     constexpr int ACT = decltype(act_c)::value;
     const int el = opaque(lane);
     const int li = el & (MR - 1), lg = el / MR;
+    Ahead now, next;
+    ahead(t, 0, li, lg, next);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
+      now = next;
+      if (i + 1 < FM) ahead(t, i + 1, li, lg, next);
       const int64_t lrow = t.row_begin + wm * TM + i * MR + li;
       const bool row_ok = lrow < t.row_end;
       if constexpr (OUT == GEMM_OUT_GEGLU) {
@@ -859,7 +895,6 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
         }
       } else if constexpr (OUT == GEMM_OUT_DGLU_SAVED) {
         // the accumulator is dm = dy Wd, in fp32; g and u as the forward kept them
-        const int64_t nb = (N + kCkptBlock - 1) / kCkptBlock;
 #pragma unroll
         for (int q = 0; q < RUNS; ++q) {
           const int64_t n = t.n0 + wn * TN + run_col(q, lg);
@@ -873,15 +908,10 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
             gst16(d2 + np, zero4());
             continue;
           }
-          const uint8_t* code = p.codes + lrow * 2 * N + n;
-          const uint8_t* sc = p.qscale + lrow * 2 * nb + n / kCkptBlock;
-          uint32_t cg[2], cu[2];
-          gld8(code, cg);
-          gld8(code + N, cu);
-          const uint32_t eg = *(const gu8_t*)sc, eu = *(const gu8_t*)(sc + nb);
+          const uint32_t cg[2] = {now.v[q][0], now.v[q][1]}, cu[2] = {now.v[q][2], now.v[q][3]};
           float g[8], u[8], m[8], dg[8], du[8];
-          ckpt_decode(cg, eg, g);
-          ckpt_decode(cu, eu, u);
+          ckpt_decode(cg, now.e[q] & 255u, g);
+          ckpt_decode(cu, now.e[q] >> 8, u);
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
             float a, da;
@@ -948,7 +978,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
             if constexpr (OUT == GEMM_OUT_DACT) {
               // the recomputed pre-activation z: dz = dy * act'(z)
               float dy[8];
-              unpack_bf16x8(gld16(p.E + lrow * p.lde + n), dy);
+              unpack_bf16x8(TRAIN ? now.v[q] : gld16(p.E + lrow * p.lde + n), dy);
 #pragma unroll
               for (int r = 0; r < 8; ++r) {
                 float a, da;
