@@ -47,14 +47,14 @@
 // in wave order (deterministic).
 //
 // Activations live in LDS as records, one per chunk: hi and lo of every token in
-// operand order, their exponents, and the groups' sums.  Up to 256 of them
+// operand order, their exponents, and the groups' sums.  Up to 64 of them
 // (tokens x chunks) a block makes its own from x, while its first weights are
 // in flight; more are made once per call by a small kernel into the workspace
 // and copied to LDS.  Where all records do not fit, k is cut into slices that
 // do: each slice has its share of the blocks, the slices' sums go to the
 // workspace in fp32 and a last small kernel adds them in order.  (Streaming the
 // records through LDS beside the weights, a step at a time, made every step
-// wait for its records: 60 us against %%% for 16 tokens through 8192 -> 28672.)
+// wait for its records: 60 us against 55 us for 16 tokens through 8192 -> 28672.)
 #include <algorithm>
 
 #include "common.h"
@@ -396,6 +396,7 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
       }
     }
   };
+  constexpr int kRedLanes = M8 ? 32 : 64;
   // One output of a tile per thread o < 256: weight row o % 16, token
   // 4 ((o / 16) % 4) + (o / 64) % 4.
   const int ov = (threadIdx.x >> 6) & 3, om = 4 * g + ov;
@@ -406,7 +407,15 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
     f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + chunks * R.bytes);   // [wave][stream][lane]
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      red[(wave * NS + s) * 64 + lane] = tot[s];
+      if constexpr (M8) {   // rows m and m + 8 are one token's: the lower half wave takes both
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t t = __float_as_uint(tot[s][v]);
+          const auto h = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+          tot[s][v] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+        }
+      }
+      if (!M8 || lane < 32) red[(wave * NS + s) * kRedLanes + lane] = tot[s];
       tot[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     lds_barrier();
@@ -418,8 +427,7 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
         z[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const float* p = reinterpret_cast<const float*>(red + (w * NS + e) * 64 + lane);
-          z[e] += M8 ? p[ov] + p[ov + 32 * 4] : p[ov];   // up to 8 tokens: rows m and m + 8
+          z[e] += reinterpret_cast<const float*>(red + (w * NS + e) * kRedLanes + lane)[ov];
         }
       }
       if (cut.parts) {
@@ -507,16 +515,16 @@ __global__ __launch_bounds__(256) void w4_sum_kernel(W4Layer L, int M, W4Cut cut
 }
 
 constexpr int64_t kLdsMax = 160 * 1024;   // of a block, one a CU
-constexpr int kUnitsInside = 256;         // tokens x chunks whose records a block makes itself
+constexpr int kUnitsInside = 64;          // tokens x chunks whose records a block makes itself: one pass of its threads
 
 int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
-int64_t red_bytes(bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * 64 * 16; }
+int64_t red_bytes(int64_t M, bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * (M <= 8 ? 32 : 64) * 16; }
 
 // The k slices of a call: as few as have records that fit in LDS, of equal
 // numbers of chunks (a multiple of 4, so that every slice starts on whole steps).
 W4Cut cut_of(int64_t M, int64_t K, int G, bool dual) {
   const int64_t chunks = (K + kChunk - 1) / kChunk;
-  const int64_t fit = (kLdsMax - red_bytes(dual)) / record_of((int)M, log2_group(G)).bytes / 4 * 4;
+  const int64_t fit = (kLdsMax - red_bytes(M, dual)) / record_of((int)M, log2_group(G)).bytes / 4 * 4;
   W4Cut c{};
   const int64_t slices = (chunks + fit - 1) / fit;
   c.chunks = (int)(((chunks + slices - 1) / slices + 3) / 4 * 4);
@@ -546,7 +554,7 @@ hipError_t launch_w4(const W4Layer& L, int M, int cus, hipStream_t s) {
   const int64_t tiles = (L.N + 15) / 16;
   if (cut.slices > 1) cut.parts = reinterpret_cast<float*>(L.scratch + records);
   cut.per_slice = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cus / cut.slices));
-  const int64_t lds = std::min(chunks, cut.chunks) * (int64_t)record_of(M, GS).bytes + red_bytes(DUAL);
+  const int64_t lds = std::min(chunks, cut.chunks) * (int64_t)record_of(M, GS).bytes + red_bytes(M, DUAL);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(cut.per_slice * cut.slices)), dim3(kThreads), (unsigned)lds, s, P, M, cut);
     return hipGetLastError();

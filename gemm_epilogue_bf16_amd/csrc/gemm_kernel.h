@@ -394,7 +394,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   constexpr bool RAGK = (KM & kKmajorRagged) != 0;
   constexpr bool TRAIN = gemm_is_train<OUT, GROUPED, KM>();
   static_assert(KM == 0 || (!DUAL && !GATHER && !M32 && BM % 128 == 0 && BN % 128 == 0 && BM <= 256 && BN <= 256 &&
-                            BK == 64 && (TM == 64 || TM == 128) && TN == 64),
+                            BK == 64 && (TM == 32 || TM == 64 || TM == 128) && TN == 64),
                 "k-major operands: tiles of 128 or 256 columns, wave tiles 64 wide, 16x16x32 MFMAs, one weight set");
   static_assert(!GROUPED || KM == 0 || KM == 2, "grouped rows: only the weights k-major");
   static_assert(!RAGK || (KMA && KMB && !GROUPED), "ragged k ranges: both operands k-major");

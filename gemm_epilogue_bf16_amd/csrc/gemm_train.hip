@@ -28,25 +28,28 @@ hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p,
   if (out_kind == GEMM_OUT_BF16 && p.kmajor == 2) {
     if (p.bias != nullptr || p.act != ACT_NONE) return hipErrorInvalidValue;
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s)
-               : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s);
+               : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s);
   }
   if (p.kmajor != 0) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16)
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s)
-               : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s);
+               : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s);
   if (out_kind == GEMM_OUT_DACT)
     return by_act(p.act, [&](auto a) {
       return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s)
-                 : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s);
+                 : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_DACT, false, true, a.value>(p, s);
     });
   return hipErrorInvalidValue;
 }
 
-// 256x256 tiles of 8 waves, or 128x128 of 4 (two blocks a CU), 64-k stages
+// 256x256 tiles, or 128x128 (two blocks a CU), both of 8 waves with 64-k stages.
+// (128x128 tiles of 4 waves: a 1001-token step of the 768 -> 2056 block 118 us
+// against 109; a ring of 4 stages, one block a CU, 3001 expert rows' gradients
+// 124 against 109.)
 template <int OUT, int KM, bool GROUPED = false>
 static hipError_t launch_km(int tile, const gemm_params_t<OUT, GROUPED, KM>& p, hipStream_t s) {
   if (tile == TILE_256x256) return launch_cfg<256, 256, 2, 4, 64, 2, OUT, false, GROUPED, ACT_NONE, false, KM>(p, s);
-  if (tile == TILE_128x128) return launch_cfg<128, 128, 2, 2, 64, 2, OUT, false, GROUPED, ACT_NONE, false, KM>(p, s);
+  if (tile == TILE_128x128) return launch_cfg<128, 128, 4, 2, 64, 2, OUT, false, GROUPED, ACT_NONE, false, KM>(p, s);
   return hipErrorInvalidValue;
 }
 
@@ -84,16 +87,16 @@ hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hi
   if (out_kind == GEMM_OUT_GLU_SAVE && p.kmajor == 0)
     return by_act(p.act, [&](auto a) {
       return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s)
-                 : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s);
+                 : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_GLU_SAVE, false, false, a.value>(p, s);
     });
   if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 2)
     return by_act(p.act, [&](auto a) {
       return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value, false, 2>(p, s)
-                 : launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value, false, 2>(p, s);
+                 : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value, false, 2>(p, s);
     });
   if (out_kind == GEMM_OUT_DGLU_SAVED && p.kmajor == 0 && !big)   // weights past the k-major span, transposed
     return by_act(p.act, [&](auto a) {
-      return launch_cfg<128, 128, 2, 2, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value>(p, s);
+      return launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_DGLU_SAVED, false, false, a.value>(p, s);
     });
   return hipErrorInvalidValue;
 }

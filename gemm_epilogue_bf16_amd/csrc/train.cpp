@@ -41,7 +41,7 @@ double rounds256(int64_t tiles, int64_t stages) {
 // full rounds of 512 tiles, two to a compute unit; up to 256 have one each
 double rounds128(int64_t tiles, int64_t stages) {
   const int64_t full = tiles / 512, rest = tiles % 512;
-  return (double)full * ((double)stages + 4) + (rest == 0 ? 0 : (rest <= 256 ? 0.62 : 1.0) * (double)stages + 4);
+  return (double)full * ((double)stages + 4) + (rest == 0 ? 0 : (rest <= 256 ? 0.50 + 0.17 * (double)rest / 256 : 1.0) * (double)stages + 4);
 }
 
 struct ProductPlan {

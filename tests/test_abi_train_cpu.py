@@ -148,8 +148,8 @@ def test_glu_w4_validation(L, kw, status, msg):
 
 
 def test_w4_sizes_and_no_tokens(L):
-    # up to 256 records (tokens x chunks of 128) are made inside the kernel and need no scratch
-    assert L.fmlp_linear_w4_workspace_size(4, 8192, 64, 64) == 0
+    # up to 64 records (tokens x chunks of 128) are made inside the kernel and need no scratch
+    assert L.fmlp_linear_w4_workspace_size(1, 8192, 64, 64) == 0 and L.fmlp_linear_w4_workspace_size(4, 2048, 64, 64) == 0
     # records of 16 tokens: 32 slots of 128 bytes, 32 exponents, 16 sums a group; they fit in LDS together
     assert L.fmlp_linear_w4_workspace_size(16, 4096, 64, 64) == 8192 + 32 * (4096 + 32 + 2 * 64)
     assert L.fmlp_linear_w4_workspace_size(16, 4096, 64, 32) == 8192 + (32 * (4096 + 32 + 4 * 64) + 255) // 256 * 256
@@ -158,8 +158,8 @@ def test_w4_sizes_and_no_tokens(L):
     assert L.fmlp_linear_w4_workspace_size(0, 4096, 64, 64) == 0 and L.fmlp_linear_w4_workspace_size(4, 4096, 64, 48) == 0
     assert L.fmlp_glu_w4_workspace_size(4, 256, 128, 64) == 8192 + 1024
     assert L.fmlp_glu_w4_workspace_size(0, 256, 128, 64) == 0 and L.fmlp_glu_w4_workspace_size(17, 256, 128, 64) == 0
-    # the larger of the layers' scratch: the first's 32 chunks in two slices of 16, made inside, with two sums each
-    assert L.fmlp_glu_w4_workspace_size(16, 4096, 14336, 64) == 8192 + 16 * 14336 * 2 + 2 * 2 * 16 * 14336 * 4
+    # the larger of the layers' scratch: the first's 32 chunks in two slices of 16, with two sums each
+    assert L.fmlp_glu_w4_workspace_size(16, 4096, 14336, 64) == 8192 + 16 * 14336 * 2 + 32 * (4096 + 32 + 2 * 64) + 2 * 2 * 16 * 14336 * 4
     assert w4(L, M=0, x=None, y=None) == OK
     assert glu_w4(L, M=0, x=None, y=None, ws=None, nb=0) == OK
     assert w4(L, M=0, x=None, y=None, q=None) == E_NULL
