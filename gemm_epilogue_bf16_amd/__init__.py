@@ -41,6 +41,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -527,9 +528,9 @@ def _need(name: str, t, dtype, device: int) -> None:
 def _need_x(x) -> int:
     if not (isinstance(x, torch.Tensor) and x.is_cuda):
         _dev_tensor("x", x)
-    device = x.get_device()
-    _need("x", x, torch.bfloat16, device)
-    return device
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _dev_tensor("x", x)
+    return x.get_device()
 
 
 def _scratch(device: int, workspace, nbytes: int):
@@ -564,7 +565,7 @@ def _on(device: int, marshal, *args):
 
 def _call(x, marshal, *args):
     device = _need_x(x)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():   # a GPU tensor exists: the runtime is up
         fn, a, out, _ = marshal(device, x, *args)
         st = fn(*a)
     else:
@@ -945,32 +946,39 @@ def bind_glu_w8(x, Wgq, sg, Wuq, su, Wdq, sd, gate_act: str = "gelu_tanh", out=N
 def _w4_weight(name, q, s, z, N, K, device) -> int:
     """Checks one 4-bit weight [N, K] and returns its group size."""
     _need(name, q, torch.uint8, device)
-    _need(f"{name}'s scales", s, torch.bfloat16, device)
+    _need("scales", s, torch.bfloat16, device)
     if K % 2 or q.shape != (N, K // 2):
         raise ValueError(f"{name} must be [{N}, {K // 2}] (two codes a byte), got {tuple(q.shape)}")
     shape = s.shape
     if len(shape) != 2 or shape[0] != N or shape[1] == 0 or K % shape[1]:
         raise ValueError(f"{name}'s scales must be [{N}, {K} / group], got {tuple(shape)}")
     if z is not None:
-        _need(f"{name}'s zeros", z, torch.bfloat16, device)
+        _need("zeros", z, torch.bfloat16, device)
         if z.shape != shape:
             raise ValueError(f"{name}'s zeros must be {tuple(shape)}, got {tuple(z.shape)}")
     return K // shape[1]
 
 
+@functools.lru_cache(maxsize=1024)
+def _linear_w4_need(M, K, N, G) -> int:
+    return lib().fmlp_linear_w4_workspace_size(M, K, N, G)
+
+
 def _linear_w4_call(device, x, Wq, scales, zeros, b, act, out, workspace):
-    K, N = x.shape[-1], Wq.shape[0]
+    *lead, K = x.shape
+    N = Wq.shape[0]
     G = _w4_weight("Wq", Wq, scales, zeros, N, K, device)
     if b is not None:
         _need("b", b, torch.bfloat16, device)
         if b.shape != (N,):
             raise ValueError(f"b must be [{N}], got {tuple(b.shape)}")
-    y = _out("out", out, x.shape[:-1] + (N,), device)
-    L = lib()
-    M = x.numel() // K
-    ws, wp, wn = _scratch(device, workspace, L.fmlp_linear_w4_workspace_size(M, K, N, G))
-    return (L.fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(b), ACT[act], M, K, N, G,
-                               y.data_ptr(), wp, wn, _raw_stream(device)), y, (x, Wq, scales, zeros, b, ws))
+    y = _out("out", out, (*lead, N), device)
+    M = lead[0] if len(lead) == 1 else x.numel() // K
+    need = _linear_w4_need(M, K, N, G)
+    ws, wp, wn = _scratch(device, workspace, need) if need else (None, None, 0)
+    return (lib().fmlp_linear_w4, (x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                   None if b is None else b.data_ptr(), ACT[act], M, K, N, G, y.data_ptr(), wp, wn,
+                                   _raw_stream(device)), y, (x, Wq, scales, zeros, b, ws))
 
 
 def fmlp_linear_w4(x, Wq, scales, zeros=None, b=None, act: str = "none", out=None, workspace=None):
