@@ -279,7 +279,7 @@ __device__ __forceinline__ void ckpt_decode(const uint32_t code[2], uint32_t e12
 // grouped products with a bias of their own per group, ragged weight gradients.
 template <int OUT, bool GROUPED, int KM>
 constexpr bool gemm_is_train() {
-  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & (kKmajorRagged | kSplitC | kSplitB)) != 0 ||
+  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & (kKmajorRagged | kList | kSplitB)) != 0 ||
          (GROUPED && (OUT == GEMM_OUT_BF16 || OUT == GEMM_OUT_DACT));
 }
 template <int OUT, bool GROUPED, int KM>
@@ -358,7 +358,7 @@ __device__ __forceinline__ void make_group_tables(GroupTables<RAGGED>& t, const 
 // per MFMA) instead of v_mfma_f32_16x16x32_bf16: half the MFMA instructions
 // and half the operand register reads per flop, the same LDS bytes.
 // KM: bit 0 A, bit 1 B stored k-major, bit 2 a k range of its own for every
-// group, bit 3 two outputs, bit 4 two padded right operands (GemmParams::kmajor).
+// group, bit 3 a list of products, bit 4 two padded right operands (GemmParams::kmajor).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int R, int OUT, bool GATHER, bool GROUPED,
           int GACT = ACT_NONE, bool M32 = false, int KM = 0>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64)
@@ -431,7 +431,17 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   // of the K range, each writing its own output copy
   constexpr bool SPLITK = OUT == GEMM_OUT_F32_SCALED;
   const int KSP = SPLITK && p.ksplit > 1 ? p.ksplit : 1;
-  const int total = (RAGK ? p.groups : 1) * tiles_m * p.tiles_n * KSP;
+  constexpr bool LIST = (KM & kList) != 0;   // products over the same k range, their tiles one after another
+  static_assert(!LIST || (KMA && KMB && !SPLITK && !RAGK && OUT == GEMM_OUT_BF16), "list: dense k-major products, bf16");
+  auto tiles_of = [&](int i) -> int {   // of product i
+    if constexpr (LIST) return (int)(((p.list[i].M + BM - 1) / BM) * ((p.list[i].N + BN - 1) / BN));
+    else return 0;
+  };
+  int total = (RAGK ? p.groups : 1) * tiles_m * p.tiles_n * KSP;
+  if constexpr (LIST) {
+    total = 0;
+    for (int i = 0; i < p.products; ++i) total += tiles_of(i);
+  }
   const int G = gridDim.x, bid = blockIdx.x;
   const int xcd = bid % kNumXcd, xj = bid / kNumXcd;
   auto blocks_before = [&](int x) {   // blocks on XCDs 0 .. x-1
@@ -471,13 +481,28 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     const uint16_t* bias;
     int64_t k_begin, c_off;   // ragged: the group's first k row, its output
     int kc;                   //   and its k rows
+    int product;              // list: which
+    int64_t rows, cols;       //   its size
+    uint16_t* c;              //   and its output
   };
   auto tile_at = [&](int i) -> Tile {   // this block's i-th tile
     int tm, tn;
     const int lt = t_lo + xj + i * nbx;
     const int lg_t = RAGK ? lt / (tiles_m * p.tiles_n * KSP) : 0;   // ragged: the tile's group
-    grouped_tile((lt - lg_t * (tiles_m * p.tiles_n * KSP)) / KSP, tiles_m, p.tiles_n, p.group_m, tm, tn);
     Tile t;
+    t.product = 0;
+    t.rows = p.M;
+    t.cols = N;
+    if constexpr (LIST) {
+      int at = lt;
+      while (t.product + 1 < p.products && at >= tiles_of(t.product)) at -= tiles_of(t.product++);
+      t.rows = p.list[t.product].M;
+      t.cols = p.list[t.product].N;
+      t.c = p.list[t.product].C;
+      grouped_tile(at, (int)((t.rows + BM - 1) / BM), (int)((t.cols + BN - 1) / BN), p.group_m, tm, tn);
+    } else {
+      grouped_tile((lt - lg_t * (tiles_m * p.tiles_n * KSP)) / KSP, tiles_m, p.tiles_n, p.group_m, tm, tn);
+    }
     t.b0 = p.B0;
     t.b1 = p.B1;
     t.bias = p.bias;
@@ -504,7 +529,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
       if constexpr (DUAL) t.b1 += (int64_t)lo * p.strideB;
     } else {
       t.row_begin = (int64_t)tm * BM;
-      t.row_end = min(t.row_begin + BM, p.M);
+      t.row_end = min(t.row_begin + BM, LIST ? t.rows : p.M);
     }
     t.n0 = (int64_t)tn * OUT_N;
     t.kp = lt % KSP;
@@ -526,7 +551,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   const int ra = RPI * wave + lane / CH;      // tile row of the lane's load 0 (activation and weight)
   const int a_k = 8 * ((lane % CH) ^ swz_a<CH>(ra));   // k of the lane's chunk in a stage
   const int b_k = 8 * ((lane % CH) ^ swz_b<CH>(ra));
-  const uint32_t lda2 = (uint32_t)p.lda * 2u;
+  uint32_t lda2 = (uint32_t)p.lda * 2u;   // list: of the product being issued, as is ldb2
   const uint32_t K2 = (uint32_t)Kc * 2u;
   // offsets of the lane's load 0 within a tile (load i adds a constant number of rows)
   const uint32_t a_lane = (uint32_t)ra * lda2 + (uint32_t)a_k * 2u;
@@ -540,13 +565,25 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   constexpr int KRA = 64 / CRA * NW, KRB = 64 / CRB * NW;   // k-rows between a wave's loads
   static_assert(KM == 0 || (KRA % 16 == 0 && KRB % 16 == 0), "one chunk permutation per lane");
   const int kra0 = 64 / CRA * wave + lane / CRA, krb0 = 64 / CRB * wave + lane / CRB;
-  const uint32_t ldb2 = (uint32_t)(KMB ? p.ldb : 0) * 2u;
-  const uint32_t a_lane_km = (uint32_t)kra0 * lda2 + (uint32_t)(((lane % CRA) ^ kswz(kra0)) * 16);
-  const uint32_t b_lane_km = (uint32_t)krb0 * ldb2 + (uint32_t)(((lane % CRB) ^ kswz(krb0)) * 16);
+  uint32_t ldb2 = (uint32_t)(KMB ? p.ldb : 0) * 2u;
+  uint32_t a_lane_km = (uint32_t)kra0 * lda2 + (uint32_t)(((lane % CRA) ^ kswz(kra0)) * 16);
+  uint32_t b_lane_km = (uint32_t)krb0 * ldb2 + (uint32_t)(((lane % CRB) ^ kswz(krb0)) * 16);
   i32x4_t da, db0, db1;
   uint32_t a_gat[GATHER ? A_INS : 1];   // gather: the lane's source-row offsets in this tile
   auto issue_tile = [&](const Tile& t) {
     const int a_rows_here = (int)(t.row_end - t.row_begin);
+    if constexpr (LIST) {
+      const GemmProduct& q = p.list[t.product];
+      lda2 = (uint32_t)q.lda * 2u;
+      ldb2 = (uint32_t)q.ldb * 2u;
+      a_lane_km = (uint32_t)kra0 * lda2 + (uint32_t)(((lane % CRA) ^ kswz(kra0)) * 16);
+      b_lane_km = (uint32_t)krb0 * ldb2 + (uint32_t)(((lane % CRB) ^ kswz(krb0)) * 16);
+      da = make_desc(reinterpret_cast<uint64_t>(q.A + t.row_begin),
+                     (uint32_t)((((int64_t)Kc - 1) * q.lda + q.M - t.row_begin) * 2));
+      db0 = make_desc(reinterpret_cast<uint64_t>(q.B + t.n0), (uint32_t)((((int64_t)Kc - 1) * q.ldb + q.N - t.n0) * 2));
+      db1 = db0;
+      return;
+    }
     // k-major descriptors end at the operand's last element ((K - 1) ld +
     // width): columns past the width read the next row's (in the operand, and
     // only into accumulators that are never stored), past the last row zeros
@@ -956,7 +993,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
           const int64_t n = t.n0 + wn * TN + run_col(q, lg);
           float v[8];
           run_vals(i, q, 0, v);
-          if (!(row_ok && n < N)) continue;
+          if (!(row_ok && n < (LIST ? t.cols : N))) continue;
           if constexpr (OUT == GEMM_OUT_F32_SCALED) {
             const float sc = p.row_scale ? p.row_scale[lrow] : 1.f;
             float* dst = static_cast<float*>(p.C) + (int64_t)t.kp * p.c_kstride + (RAGK ? t.c_off : 0) + lrow * p.ldc + n;
@@ -989,10 +1026,8 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
 #pragma unroll
               for (int r = 0; r < 8; ++r) v[r] = act_of<ACT>(v[r]);
             }
-            if constexpr ((KM & kSplitC) != 0) {   // rows from c_split on are C2's; either has c_rows
-              const bool second = lrow >= p.c_split;
-              const int64_t cr = lrow - (second ? p.c_split : 0);
-              if (cr < p.c_rows) gst16(static_cast<uint16_t*>(second ? p.C2 : p.C) + cr * p.ldc + n, pack_bf16x8(v));
+            if constexpr (LIST) {
+              gst16(t.c + lrow * t.cols + n, pack_bf16x8(v));
             } else {
               gst16(static_cast<uint16_t*>(p.C) + (RAGK ? t.c_off : 0) + lrow * p.ldc + n, pack_bf16x8(v));
             }
@@ -1173,8 +1208,17 @@ hipError_t launch_cfg(gemm_params_t<OUT, GROUPED, KM> p, hipStream_t s) {
   if (!GROUPED) p.tiles_m = (int)((p.M + BM - 1) / BM);
   p.tiles_n = (int)((p.N + OUT_N - 1) / OUT_N);
   p.group_m = 4;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * ((KM & kKmajorRagged) ? p.groups : 1) *   // grouped: an upper bound
+  int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * ((KM & kKmajorRagged) ? p.groups : 1) *   // grouped: an upper bound
                         ((OUT == GEMM_OUT_F32_SCALED && p.ksplit > 1) ? p.ksplit : 1);
+  if constexpr ((KM & kList) != 0) {
+    if (p.products < 1 || p.products > kMaxProducts) return hipErrorInvalidValue;
+    tiles = 0;
+    for (int i = 0; i < p.products; ++i) {
+      const GemmProduct& q = p.list[i];
+      if (std::max(q.lda, q.ldb) * p.K * 2 >= (int64_t(1) << 31) || q.lda < q.M || q.ldb < q.N) return hipErrorInvalidValue;
+      tiles += ((q.M + BM - 1) / BM) * ((q.N + BN - 1) / BN);
+    }
+  }
   if (tiles <= 0) return hipSuccess;
   if (tiles > 0x7fffffff || p.cus <= 0) return hipErrorInvalidValue;
   // A 32-k stage tile consumes its stages two at a time, so it needs an even

@@ -22,10 +22,15 @@ constexpr int kCkptBlock = 32;
 constexpr int kKmajorRagged = 4;
 constexpr int kMaxGroups = 1024;
 
-// bit 3: rows [0, c_rows) of the output go to C, rows [c_split, c_split + c_rows)
-// to C2 (bf16, both with row stride ldc), the others nowhere: two weight gradients
-// with the same right operand in one launch.
-constexpr int kSplitC = 8;
+// bit 3: a list of products over the same k rows (K), each with operands, sizes and
+// a bf16 output [M, N] of its own: weight gradients of one step in one launch.
+constexpr int kList = 8;
+constexpr int kMaxProducts = 3;
+struct GemmProduct {
+  const uint16_t *A, *B;   // k-major [K, lda] (the output's rows are columns of A), [K, ldb]
+  uint16_t* C;             // row stride N
+  int64_t lda, ldb, M, N;
+};
 // bit 4, with kb_split: B0 and B1 have kb_rows (at most kb_split) rows each, and
 // the k rows from there to the split (or to K) are zeros.
 constexpr int kSplitB = 16;
@@ -34,7 +39,8 @@ struct GemmTrainParams : GemmParams {
   uint8_t* codes;              // checkpoint: E4M3 codes [rows, 2N], g in columns [0, N), u in [N, 2N)
   uint8_t* qscale;             // and scale exponents (+ 127) [rows, 2 ceil(N / kCkptBlock)]
   int64_t stride_bias;         // grouped: elements between consecutive groups' biases
-  int64_t c_split, c_rows;     // kSplitC
+  int products;                // kList
+  GemmProduct list[kMaxProducts];
   int64_t kb_rows;             // kSplitB
   int64_t stride_c;            // ragged: elements between consecutive groups' outputs
   int64_t group_rows;          // grouped, ragged: the rows there are; group_off is the caller's table, unchecked
@@ -47,7 +53,7 @@ hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p,
 // The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
 hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // Dense products on either tile, bf16 or split fp32: kmajor = 0, 2 | kSplitB, 3 or
-// 3 | kSplitC (bf16 only).
+// 3 | kList (bf16 only).
 hipError_t launch_gemm_kmajor(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // GEMM_OUT_GLU_SAVE, and GEMM_OUT_DGLU_SAVED (kmajor 0 or 2).
 hipError_t launch_gemm_ckpt(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);

@@ -70,7 +70,7 @@ hipError_t launch_gemm_kmajor(int out_kind, int tile, const GemmTrainParams& p, 
     if (p.kmajor == 0) return launch_km<GEMM_OUT_BF16, 0>(tile, p, s);
     if (p.kmajor == (2 | kSplitB)) return launch_km<GEMM_OUT_BF16, 2 | kSplitB>(tile, p, s);
     if (p.kmajor == 3) return launch_km<GEMM_OUT_BF16, 3>(tile, p, s);
-    if (p.kmajor == (3 | kSplitC) && p.C2 != nullptr) return launch_km<GEMM_OUT_BF16, 3 | kSplitC>(tile, p, s);
+    if (p.kmajor == (3 | kList)) return launch_km<GEMM_OUT_BF16, 3 | kList>(tile, p, s);
   }
   if (out_kind == GEMM_OUT_F32_SCALED) {
     if (p.kmajor == 0) return launch_km<GEMM_OUT_F32_SCALED, 0>(tile, p, s);

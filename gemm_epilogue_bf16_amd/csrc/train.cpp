@@ -46,22 +46,19 @@ double rounds128(int64_t tiles, int64_t stages) {
 
 struct ProductPlan {
   int tile, split;
+  double us;
 };
 // tiles256, tiles128: the product's tiles of either size, `stages` of 64 k each;
 // out: its output elements; max_split: 1 where k cannot be split.
 ProductPlan plan_product(int64_t tiles256, int64_t tiles128, int64_t stages, int64_t out, int max_split) {
-  ProductPlan best{TILE_256x256, 1};
-  double least = 0;
+  ProductPlan best{TILE_256x256, 1, 0};
   for (int P = 1; P <= max_split; ++P) {
     if (P > 1 && stages / P < 4) break;
     const double parts = P > 1 ? kPartsLaunch + 8.0 * P * (double)out / kPartsBytesPerUs : 0;
     for (int tile : {TILE_256x256, TILE_128x128}) {
       const int64_t st = (stages + P - 1) / P;
       const double t = (tile == TILE_256x256 ? rounds256(tiles256 * P, st) : rounds128(tiles128 * P, st)) + parts;
-      if (least == 0 || t < least) {
-        least = t;
-        best = {tile, P};
-      }
+      if (best.us == 0 || t < best.us) best = {tile, P, t};
     }
   }
   return best;
@@ -75,27 +72,17 @@ size_t parts_bytes(const ProductPlan& p, int64_t out) {
   return p.split > 1 ? round_up((size_t)p.split * (size_t)out * 4, 256) : 0;
 }
 
-// A product on its plan: C = A . B with the operands of `kmajor`; with C2, rows
-// [0, rows) of it are C's and rows [at, at + rows) C2's.
-hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, uint16_t* C2, int64_t at, int64_t rows,
-                       float* parts, hipStream_t s) {
+// A product on its plan: C [M, N] = A . B with the operands of `kmajor`.
+hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, float* parts, hipStream_t s) {
   if (plan.split == 1) {
     p.C = C;
-    if (C2) {
-      p.C2 = C2;
-      p.c_split = at;
-      p.c_rows = rows;
-      p.kmajor |= kSplitC;
-    }
     return launch_gemm_kmajor(GEMM_OUT_BF16, plan.tile, p, s);
   }
   p.C = parts;
   p.ksplit = plan.split;
   p.c_kstride = p.M * p.N;
-  hipError_t e = launch_gemm_kmajor(GEMM_OUT_F32_SCALED, plan.tile, p, s);
-  if (e == hipSuccess) e = launch_sum_parts(parts, plan.split, p.M * p.N, (C2 ? rows : p.M) * p.N, C, s);
-  if (e == hipSuccess && C2) e = launch_sum_parts(parts + at * p.N, plan.split, p.M * p.N, rows * p.N, C2, s);
-  return e;
+  const hipError_t e = launch_gemm_kmajor(GEMM_OUT_F32_SCALED, plan.tile, p, s);
+  return e != hipSuccess ? e : launch_sum_parts(parts, plan.split, p.M * p.N, p.M * p.N, C, s);
 }
 
 // The row tiles of E ragged groups: the sizes are on the device, so the mean
@@ -281,20 +268,23 @@ fmlp_status fmlp_glu_ckpt(const fmlp_bf16* x, const fmlp_bf16* Wg, const fmlp_bf
   HIP_TRY(launch_gemm_ckpt(GEMM_OUT_GLU_SAVE, plan_dense(M, 2 * H, D, 1).tile, p, s), "glu_ckpt gate+up launch");
   p = train_params(dense_params(m, H, Wd, nullptr, nullptr, nullptr, D, M, D, H, FMLP_ACT_NONE, cus));
   float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader + ws_bf16(M, H));
-  return launched(run_product(plan_dense(M, D, H), p, y, nullptr, 0, 0, parts, s), "glu_ckpt down launch");
+  return launched(run_product(plan_dense(M, D, H), p, y, parts, s), "glu_ckpt down launch");
 }
 
 namespace {
 // The products of the checkpoint's backward, all with operands as stored (read
-// k-major): dm [M, H] over D, dx [M, D] over 2H, dWd [D, H] and dWg | dWu [2H, D]
-// over the tokens.  `stored`: the spans fit (operands below 2^30 elements);
+// k-major): dm [M, H] over D, dx [M, D] over 2H, dWd [D, H], dWg and dWu [H, D] over
+// the tokens.  The weight gradients run as one list of tiles in one launch where
+// that saves rounds, else dWd and a list of dWg and dWu, or each by itself where few
+// tiles over many tokens are better split.  `stored`: the spans fit (operands below 2^30 elements);
 // else the transposing form of fmlp_glu_bwd's last steps.
 // dg and du are Hp columns wide, H rounded up to the 64-k stages of dx's product,
 // with zeros in between.
 struct CkptBwdLayout {
   bool stored;
   int64_t Hp;
-  ProductPlan dm, dx, dwd, dwgu;
+  ProductPlan dm, dx, dw3, dw2, dwd, dwgu;   // dw3: a list of all three gradients; dw2: of dWg and dWu
+  int listed;                                 // 3, 2 (dWd by itself) or 0
   size_t m, dgdu, scratch, total;
 };
 CkptBwdLayout ckpt_bwd_layout(int64_t M, int64_t D, int64_t H) {
@@ -305,12 +295,24 @@ CkptBwdLayout ckpt_bwd_layout(int64_t M, int64_t D, int64_t H) {
   L.dm = plan_dense(M, H, D, 1);   // its epilogue needs the whole sum
   L.dx = plan_dense(M, D, 2 * L.Hp);
   L.dwd = plan_dense(D, H, M);
-  L.dwgu = plan_dense(2 * L.Hp, D, M);
+  L.dwgu = plan_dense(H, D, M);
+  L.dw2 = plan_product(2 * tiles_of(H, D, 256), 2 * tiles_of(H, D, 128), (M + 63) / 64, 2 * D * H, 1);
+  L.dw3 = plan_product(tiles_of(D, H, 256) + 2 * tiles_of(H, D, 256), tiles_of(D, H, 128) + 2 * tiles_of(H, D, 128),
+                       (M + 63) / 64, 3 * D * H, 1);
+  // us of a launch's start and end.  A list's sizes and pointers change from tile to
+  // tile, and the long one has all five operands in flight at once on different
+  // XCDs and reads them more often: at 4096 tokens of 8192 -> 28672, where every
+  // form has the same rounds, 9.06 ms as one list of three and 9.0 with a list of
+  // two, 8.9 without; at 1001 tokens of 768 -> 2056 one list takes 98 us, two launches 109.
+  constexpr double kLaunch = 3.0, kList2 = 1.02, kList3 = 1.1;
+  const double one = 2 * L.dwgu.us + kLaunch, two = kList2 * L.dw2.us;
+  L.listed = kList3 * L.dw3.us < L.dwd.us + kLaunch + std::min(one, two) ? 3 : two < one ? 2 : 0;
   size_t o = kHeader;
   L.m = o;       o += ws_bf16(M, H);
   L.dgdu = o;    o += ws_bf16(M, 2 * L.Hp);
   L.scratch = o;   // the parts of split products, one at a time, or the transposes
-  o += L.stored ? std::max({parts_bytes(L.dx, M * D), parts_bytes(L.dwd, D * H), parts_bytes(L.dwgu, 2 * L.Hp * D)})
+  o += L.stored ? std::max({parts_bytes(L.dx, M * D), L.listed == 3 ? 0 : parts_bytes(L.dwd, D * H),
+                          L.listed ? 0 : parts_bytes(L.dwgu, H * D)})
                 : std::max(ws_bf16(H, D), glu_products_scratch(M, D, H));
   L.total = o;
   return L;
@@ -381,16 +383,27 @@ fmlp_status fmlp_glu_ckpt_bwd(const fmlp_bf16* x, const fmlp_fp8* codes, const u
   q.ldb = D;
   q.kb_split = L.Hp;
   q.kb_rows = H;
-  HIP_TRY(run_product(L.dx, q, dx, nullptr, 0, 0, parts, s), "glu_ckpt_bwd dx launch");
-  q = train_params(dense_params(dy, D, m, nullptr, nullptr, nullptr, H, D, H, M, FMLP_ACT_NONE, cus));
-  q.kmajor = 3;
-  q.ldb = H;
-  HIP_TRY(run_product(L.dwd, q, dWd, nullptr, 0, 0, parts, s), "glu_ckpt_bwd dWd launch");
-  // dWg | dWu = [dg | du]^T x: one product of 2 Hp rows
-  q = train_params(dense_params(dgdu, 2 * L.Hp, x, nullptr, nullptr, nullptr, D, 2 * L.Hp, D, M, FMLP_ACT_NONE, cus));
-  q.kmajor = 3;
-  q.ldb = D;
-  HIP_TRY(run_product(L.dwgu, q, dWg, dWu, L.Hp, H, parts, s), "glu_ckpt_bwd dWg, dWu launch");
+  HIP_TRY(run_product(L.dx, q, dx, parts, s), "glu_ckpt_bwd dx launch");
+  const GemmProduct dw[3] = {{dy, m, dWd, D, H, D, H},
+                             {dgdu, x, dWg, 2 * L.Hp, D, H, D},
+                             {dgdu + L.Hp, x, dWu, 2 * L.Hp, D, H, D}};
+  for (int i = 0; i < 3 - L.listed; ++i) {
+    const GemmProduct& w = dw[i];
+    q = train_params(dense_params(w.A, w.lda, w.B, nullptr, nullptr, nullptr, w.N, w.M, w.N, M, FMLP_ACT_NONE, cus));
+    q.kmajor = 3;
+    q.ldb = w.ldb;
+    HIP_TRY(run_product(i == 0 ? L.dwd : L.dwgu, q, w.C, parts, s), "glu_ckpt_bwd weight gradient launch");
+  }
+  if (L.listed) {
+    const GemmProduct& w = dw[3 - L.listed];
+    q = train_params(dense_params(w.A, w.lda, w.B, nullptr, nullptr, nullptr, w.N, w.M, w.N, M, FMLP_ACT_NONE, cus));
+    q.kmajor = 3 | kList;
+    q.ldb = w.ldb;
+    q.products = L.listed;
+    std::copy(dw + 3 - L.listed, dw + 3, q.list);
+    HIP_TRY(launch_gemm_kmajor(GEMM_OUT_BF16, L.listed == 3 ? L.dw3.tile : L.dw2.tile, q, s),
+            "glu_ckpt_bwd weight gradients launch");
+  }
   return ok();
 }
 
