@@ -92,6 +92,29 @@ def test_large_tiles_and_split_products():
         ffn64.check(n, a, w, e)
 
 
+# the weight gradients in one launch, with either tile, in two, and in three
+@pytest.mark.parametrize("M,D,H", [(300, 512, 1000), (601, 776, 3080), (600, 1032, 5128), (2100, 2056, 5128)])
+def test_weight_gradients_of_every_form(M, D, H):
+    gradients_at(M, D, H, "relu")
+
+
+def test_operands_past_31_bits():
+    """dg and du together span 2^31 bytes: their products read rewritten copies"""
+    gradients_at(65536 + 8, 8, 8192, "silu")
+
+
+def gradients_at(M, D, H, act):
+    import gemm_epilogue_bf16_amd as F
+
+    t = make(M, D, H, seed=9)
+    d = {k: v.double() for k, v in t.items()}
+    _, codes, scales = F.fmlp_glu_ckpt(t["x"], t["Wg"], t["Wu"], t["Wd"], act)
+    got = F.fmlp_glu_ckpt_bwd(t["x"], codes, scales, t["Wg"], t["Wu"], t["Wd"], act, t["dy"])
+    want, bound = ffn64.glu_bwd_at(*ffn64.ckpt_values(codes, scales), d["x"], d["Wg"], d["Wu"], d["Wd"], act, d["dy"])
+    for n, a, w, e in zip(("dx", "dWg", "dWu", "dWd"), got, want, bound):
+        ffn64.check(n, a, w, e)
+
+
 def test_codes_of_every_value():
     """The backward reads every finite code and scales over their range: g takes all 254 finite codes, at scales from
     2^-20 to 2^3, with u = 1.  dm = dy Wd is then seen through du = dm act(g) (act none: g itself) exactly."""
