@@ -653,7 +653,7 @@ def _ckpt_args(device, x, Wg, Wu, Wd):
     D, H = x.shape[-1], Wg.shape[0]
     if Wg.shape != (H, D) or Wu.shape != (H, D) or Wd.shape != (D, H):
         raise ValueError(f"shape mismatch: x[...,{D}] Wg{tuple(Wg.shape)} Wu{tuple(Wu.shape)} Wd{tuple(Wd.shape)}")
-    return x.numel() // D, D, H
+    return (x.numel() // D if D else 0), D, H
 
 
 def _glu_ckpt_call(device, x, Wg, Wu, Wd, gate_act, out, workspace):

@@ -40,11 +40,11 @@
 // each carries half of the zero point's sum); beyond, a second MFMA takes lo.
 // A 16-byte load gives a lane 32 consecutive codes of its row.
 //
-// A block's 8 waves are WR row tiles (16 rows each, gate and up rows for a
-// gated layer) times WK parts of k.  The grid is persistent (two blocks a CU)
-// and a block's work is one stream of steps (U chunks per wave) through its
-// tiles, with two steps' weights in flight in registers, across tiles.  Partial sums of the WK waves meet in LDS
-// in wave order (deterministic).
+// A block has 16 waves and a CU to itself (the grid is persistent); they share a
+// tile of 16 rows (gate and up rows for a gated layer), U chunks of k each a
+// step.  A block's work is one stream of steps through its tiles, with two
+// steps' weights in flight in registers, across tiles.  The 16 waves' sums meet in
+// LDS in wave order (deterministic).
 //
 // Activations live in LDS as records, one per chunk: hi and lo of every token in
 // operand order, their exponents, and the groups' sums.  Up to 64 of them
@@ -55,6 +55,12 @@
 // workspace in fp32 and a last small kernel adds them in order.  (Streaming the
 // records through LDS beside the weights, a step at a time, made every step
 // wait for its records: 60 us against 55 us for 16 tokens through 8192 -> 28672.)
+//
+// What it reaches (GPU time in a replayed graph).  A call of many tiles takes about
+// 8 us (start, records, first loads, last sums) and then reads 5.7 TB/s, where a
+// copy moves 5.15.  One token through 4096 -> 4096 takes 4.6 us, through the gated
+// 8192 -> 28672 -> 8192 block 80 us (363 MB, 4.5 TB/s), 16 tokens through
+// 8192 -> 28672 47 to 55 us (148 MB; two slices of k, three launches).
 #include <algorithm>
 
 #include "common.h"

@@ -103,6 +103,23 @@ def test_operands_past_31_bits():
     gradients_at(65536 + 8, 8, 8192, "silu")
 
 
+def test_forward_past_32_bits():
+    """2^32 codes and more: the rows at the end"""
+    import gemm_epilogue_bf16_amd as F
+
+    M, D, H = (1 << 19) + 200, 16, 4096
+    t = make(M, D, H, seed=10)
+    y, codes, scales = F.fmlp_glu_ckpt(t["x"], t["Wg"], t["Wu"], t["Wd"], "silu")
+    r = slice(M - 300, M)
+    d = {k: v.double() for k, v in t.items() if k != "dy"}
+    want, bound = ffn64.glu(d["x"][r], d["Wg"], d["Wu"], d["Wd"], "silu")
+    ffn64.check("y", y[r], want, bound)
+    nb = scales.shape[1] // 2
+    for i, W in enumerate((d["Wg"], d["Wu"])):
+        v, ev = ffn64.mm(d["x"][r], W.t())
+        check_stored(v, ev, codes[r, i * H:(i + 1) * H], scales[r, i * nb:(i + 1) * nb])
+
+
 def gradients_at(M, D, H, act):
     import gemm_epilogue_bf16_amd as F
 

@@ -119,6 +119,21 @@ def test_many_groups():
         ffn64.check(n, a, w, e)
 
 
+def test_offsets_past_32_bits():
+    """2^32 output elements and more: the rows at the end"""
+    import gemm_epilogue_bf16_amd as F
+
+    K, N, R = 32, 4096, (1 << 20) + 300
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(R, K, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(3, N, K, generator=g, device="cuda") / K ** 0.5).bfloat16()
+    off = torch.tensor([0, 100, R - 257, R], dtype=torch.int32, device="cuda")
+    y = F.fmlp_grouped_linear(x, off, W, None, "silu")
+    for r, e in ((slice(0, 100), 0), (slice(R - 600, R - 257), 1), (slice(R - 257, R), 2)):
+        want, bound = ffn64.grouped(x[r].double(), [0, r.stop - r.start], W[e:e + 1].double(), None, "silu")
+        ffn64.check(f"group {e}", y[r], want, bound)
+
+
 def test_infinities_stay_in_their_group():
     import gemm_epilogue_bf16_amd as F
 

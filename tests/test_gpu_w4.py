@@ -43,6 +43,17 @@ def test_linear(M, K, N, G, zeros):
         ffn64.check(act, F.fmlp_linear_w4(x, *w, bias, act), want, ffn64.rounded(want, ffn64.act_err(zz, ez, act)[0]))
 
 
+@pytest.mark.parametrize("M,K,N,G", [(1, 262144, 24, 64), (16, 65536, 40, 32), (9, 1048576, 8, 128)])
+def test_long_rows_in_many_slices(M, K, N, G):
+    import gemm_epilogue_bf16_amd as F
+
+    g = gen(K)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    w = weight(g, N, K, G, True)
+    want, e = ffn64.w4_linear(x.double(), None, *w)
+    ffn64.check("y", F.fmlp_linear_w4(x, *w), want, ffn64.rounded(want, e))
+
+
 @pytest.mark.parametrize("M,D,H,G", [(1, 32, 64, 32), (2, 96, 160, 32), (16, 128, 256, 128), (5, 320, 448, 64),
                                      (1, 4096, 1024, 128), (16, 4096, 1152, 128), (3, 1056, 4128, 32), (16, 2112, 4160, 64)])
 @pytest.mark.parametrize("zeros", [(False, False), (True, True), (True, False), (False, True)])
