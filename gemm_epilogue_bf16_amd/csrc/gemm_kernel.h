@@ -279,7 +279,7 @@ __device__ __forceinline__ void ckpt_decode(const uint32_t code[2], uint32_t e12
 // grouped products with a bias of their own per group, ragged weight gradients.
 template <int OUT, bool GROUPED, int KM>
 constexpr bool gemm_is_train() {
-  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & (kKmajorRagged | kList | kSplitB)) != 0 ||
+  return OUT == GEMM_OUT_GLU_SAVE || OUT == GEMM_OUT_DGLU_SAVED || (KM & (kKmajorRagged | kList | kSplitB | kTail)) != 0 ||
          (GROUPED && (OUT == GEMM_OUT_BF16 || OUT == GEMM_OUT_DACT));
 }
 template <int OUT, bool GROUPED, int KM>
@@ -349,6 +349,24 @@ __device__ __forceinline__ void make_group_tables(GroupTables<RAGGED>& t, const 
   __syncthreads();
 }
 
+// The blocks of a persistent grid of G on XCDs 0 .. x - 1 (block b is on XCD b mod 8).
+__device__ __forceinline__ int blocks_before_xcd(int G, int x) {
+  const int q = G / kNumXcd, r = G % kNumXcd;
+  return x * q + min(x, r);
+}
+// kTail: how an XCD's n tiles run on its nb blocks: whole rounds, then `rest` tiles
+// in `parts` parts of the k range each, one per block (1: the rest runs unsplit).
+struct TailCut {
+  int full, rest, parts;
+};
+__device__ __forceinline__ TailCut tail_cut(int n, int nb) {
+  TailCut c;
+  c.full = n / nb * nb;
+  c.rest = n - c.full;
+  c.parts = c.rest > 0 ? min(nb / c.rest, kMaxTailParts) : 1;
+  return c;
+}
+
 // GACT: the gate activation of a gated (GEMM_OUT_GEGLU, GEMM_OUT_DGLU) kernel,
 // or the activation of a GEMM_OUT_DACT kernel, fixed per kernel so each
 // carries one epilogue: with several epilogue copies behind a
@@ -358,7 +376,8 @@ __device__ __forceinline__ void make_group_tables(GroupTables<RAGGED>& t, const 
 // per MFMA) instead of v_mfma_f32_16x16x32_bf16: half the MFMA instructions
 // and half the operand register reads per flop, the same LDS bytes.
 // KM: bit 0 A, bit 1 B stored k-major, bit 2 a k range of its own for every
-// group, bit 3 a list of products, bit 4 two padded right operands (GemmParams::kmajor).
+// group, bit 3 a list of products, bit 4 two padded right operands, bit 5 the last
+// round's tiles split over K (GemmParams::kmajor).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int BK, int R, int OUT, bool GATHER, bool GROUPED,
           int GACT = ACT_NONE, bool M32 = false, int KM = 0>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64)
@@ -396,7 +415,9 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   static_assert(KM == 0 || (!DUAL && !GATHER && !M32 && BM % 128 == 0 && BN % 128 == 0 && BM <= 256 && BN <= 256 &&
                             BK == 64 && (TM == 32 || TM == 64 || TM == 128) && TN == 64),
                 "k-major operands: tiles of 128 or 256 columns, wave tiles 64 wide, 16x16x32 MFMAs, one weight set");
-  static_assert(!GROUPED || KM == 0 || KM == 2, "grouped rows: only the weights k-major");
+  constexpr bool TAIL = (KM & kTail) != 0;
+  static_assert(!GROUPED || (KM & ~kTail) == 0 || (KM & ~kTail) == 2, "grouped rows: only the weights k-major");
+  static_assert(!TAIL || (GROUPED && OUT == GEMM_OUT_BF16), "split last round: grouped rows, bf16");
   static_assert(!RAGK || (KMA && KMB && !GROUPED), "ragged k ranges: both operands k-major");
   static_assert(!(OUT == GEMM_OUT_GLU_SAVE && M32) && kCkptBlock == 32, "a checkpoint block is one run of 4 lane groups");
 
@@ -444,10 +465,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   }
   const int G = gridDim.x, bid = blockIdx.x;
   const int xcd = bid % kNumXcd, xj = bid / kNumXcd;
-  auto blocks_before = [&](int x) {   // blocks on XCDs 0 .. x-1
-    const int q = G / kNumXcd, r = G % kNumXcd;
-    return x * q + min(x, r);
-  };
+  auto blocks_before = [&](int x) { return blocks_before_xcd(G, x); };   // blocks on XCDs 0 .. x-1
   const int nbx = blocks_before(xcd + 1) - blocks_before(xcd);
   // Ragged k ranges: tiles cost what their group's k rows are, so the XCDs'
   // ranges are cut at equal stages instead of equal tiles (8 groups over 8
@@ -470,12 +488,18 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   };
   const int t_lo = range_end(xcd);
   const int t_hi = range_end(xcd + 1);
-  const int nmine = xj < t_hi - t_lo ? (t_hi - t_lo - xj + nbx - 1) / nbx : 0;
+  int nmine = xj < t_hi - t_lo ? (t_hi - t_lo - xj + nbx - 1) / nbx : 0;
+  TailCut cut{0, 0, 1};
+  if constexpr (TAIL) {
+    cut = tail_cut(t_hi - t_lo, nbx);
+    nmine = cut.full / nbx + (xj < cut.rest * cut.parts ? 1 : 0);
+  }
   if (nmine == 0) return;   // block-uniform: no barrier has been reached
 
   struct Tile {
     int64_t row_begin, row_end, n0;
     int kp;   // part of the K range (split-K)
+    int parts;   // tail: of so many
     const uint16_t* b0;
     const uint16_t* b1;
     const uint16_t* bias;
@@ -487,7 +511,9 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   };
   auto tile_at = [&](int i) -> Tile {   // this block's i-th tile
     int tm, tn;
-    const int lt = t_lo + xj + i * nbx;
+    int lt = t_lo + xj + i * nbx;
+    const bool tail = TAIL && cut.parts > 1 && i * nbx == cut.full;
+    if (tail) lt = t_lo + cut.full + xj / cut.parts;
     const int lg_t = RAGK ? lt / (tiles_m * p.tiles_n * KSP) : 0;   // ragged: the tile's group
     Tile t;
     t.product = 0;
@@ -533,6 +559,11 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     }
     t.n0 = (int64_t)tn * OUT_N;
     t.kp = lt % KSP;
+    t.parts = 1;
+    if (tail) {
+      t.kp = xj % cut.parts;
+      t.parts = cut.parts;
+    }
     return t;
   };
 
@@ -637,18 +668,21 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   // part without any (an empty group, or fewer stages than parts) runs one
   // stage of zeros, so its output is written.
   auto rag_first = [&](const Tile& t, int kp) { return (int)((int64_t)kp * ((t.kc + BK - 1) / BK) / KSP); };
+  auto tail_first = [&](const Tile& t, int kp) { return kp * nk / t.parts; };
   auto stages_of = [&](const Tile& t) -> int {
-    if constexpr (RAGK) return max(rag_first(t, t.kp + 1) - rag_first(t, t.kp), 1);
+    if constexpr (TAIL) return tail_first(t, t.kp + 1) - tail_first(t, t.kp);
+    else if constexpr (RAGK) return max(rag_first(t, t.kp + 1) - rag_first(t, t.kp), 1);
     else return part_stages(t.kp);
   };
   int iss_kp = 0;   // K part of the tile whose stages are being issued
   int iss_ns = NS;  // and its stage count
-  int iss_kc = Kc;  // ragged: the k rows of its group (none for a part of zeros) and its first stage
+  int iss_kc = Kc;  // ragged: the k rows of its group (none for a part of zeros); ragged, tail: its first stage
   int iss_first = 0;
   auto iss_begin = [&](const Tile& t) {
     issue_tile(t);
     iss_kp = t.kp;
     iss_ns = stages_of(t);
+    if constexpr (TAIL) iss_first = tail_first(t, t.kp);
     if constexpr (RAGK) {
       iss_first = rag_first(t, t.kp);
       iss_kc = rag_first(t, t.kp + 1) > iss_first ? t.kc : 0;
@@ -674,7 +708,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   auto stage_begin = [&]() -> StageIssue {
     const bool live = iss_t < nmine;   // block-uniform
     if (live && iss_s == 0 && iss_t > 0) iss_begin(tile_at(iss_t));
-    const int first = RAGK ? iss_first : SPLITK ? part_first(iss_kp) : 0;
+    const int first = RAGK || TAIL ? iss_first : SPLITK ? part_first(iss_kp) : 0;
     const int ks0 = __builtin_amdgcn_readfirstlane(live ? first + iss_s : 0);   // stage index within K
     const int kc = RAGK ? iss_kc : Kc;
     const int k0 = live ? ks0 * BK : kc;
@@ -994,6 +1028,20 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
           float v[8];
           run_vals(i, q, 0, v);
           if (!(row_ok && n < (LIST ? t.cols : N))) continue;
+          if constexpr (TAIL) {   // a part of a tail tile: its fp32 sum, for gemm_tail_kernel
+            if (t.parts > 1) {
+              float* dst = p.tail + (int64_t)bid * (BM * BN) + (lrow - t.row_begin) * BN + (n - t.n0);
+              u32x4_t lo, hi;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                lo[r] = __float_as_uint(v[r]);
+                hi[r] = __float_as_uint(v[4 + r]);
+              }
+              gst16(dst, lo);
+              gst16(dst + 4, hi);
+              continue;
+            }
+          }
           if constexpr (OUT == GEMM_OUT_F32_SCALED) {
             const float sc = p.row_scale ? p.row_scale[lrow] : 1.f;
             float* dst = static_cast<float*>(p.C) + (int64_t)t.kp * p.c_kstride + (RAGK ? t.c_off : 0) + lrow * p.ldc + n;
@@ -1177,7 +1225,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   using K0 = std::integral_constant<int, 0>;
   int slot = 0;
   for (int ti = 0; ti < nmine; ++ti) {
-    const int ns = SPLITK || RAGK ? stages_of(tile_at(ti)) : NS;
+    const int ns = SPLITK || RAGK || TAIL ? stages_of(tile_at(ti)) : NS;
     if constexpr (KS >= 2) {
       for (int q = 0; q < ns - 1; ++q) {
         stage(slot, Mid{});
@@ -1199,6 +1247,50 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
     slot = next_slot(slot);
   }
   wait_vm<0>();   // the stages issued past the end (loads of nothing) land before LDS is released
+}
+
+// kTail's second launch, with the first one's grid: the block that made part kp of a
+// split tile adds a share of the tile's rows over its parts, in their order, and
+// rounds once.
+template <int BM, int BN>
+__global__ void __launch_bounds__(512) gemm_tail_kernel(GemmTrainParams p) {
+  __shared__ GroupTables<false> tables;
+  make_group_tables(tables, p.group_off, p.groups, (int32_t)p.group_rows, BM, 1);
+  const int G = gridDim.x, bid = blockIdx.x;
+  const int xcd = bid % kNumXcd, xj = bid / kNumXcd;
+  const int tiles_m = tables.tile[p.groups];
+  const int64_t total = (int64_t)tiles_m * p.tiles_n;
+  const int b0 = blocks_before_xcd(G, xcd), b1 = blocks_before_xcd(G, xcd + 1);
+  const int t_lo = (int)(total * b0 / G), t_hi = (int)(total * b1 / G);
+  const TailCut cut = tail_cut(t_hi - t_lo, b1 - b0);
+  if (cut.parts == 1 || xj >= cut.rest * cut.parts) return;
+  int tm, tn;
+  grouped_tile(t_lo + cut.full + xj / cut.parts, tiles_m, p.tiles_n, p.group_m, tm, tn);
+  int lo = 0, hi = p.groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tables.tile[mid] <= tm) lo = mid; else hi = mid;
+  }
+  const int64_t row0 = (int64_t)tables.off[lo] + (int64_t)(tm - tables.tile[lo]) * BM;
+  const int rows = (int)min((int64_t)BM, tables.off[lo + 1] - row0);
+  const int kp = xj % cut.parts, first = xj - kp;   // the tile's parts: blocks first .. of this XCD
+  const int c = (threadIdx.x % (BN / 8)) * 8;
+  const int64_t n = (int64_t)tn * BN + c;
+  if (n >= p.N) return;   // N % 8 == 0
+  const int end = min(rows, (kp + 1) * BM / cut.parts);
+  for (int r = kp * BM / cut.parts + threadIdx.x / (BN / 8); r < end; r += 512 / (BN / 8)) {
+    float v[8] = {};
+    for (int j = 0; j < cut.parts; ++j) {
+      const float* src = p.tail + (int64_t)(xcd + kNumXcd * (first + j)) * (BM * BN) + r * BN + c;
+      const u32x4_t a = ld16(src), b = ld16(src + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += __uint_as_float(a[e]);
+        v[4 + e] += __uint_as_float(b[e]);
+      }
+    }
+    st16(static_cast<uint16_t*>(p.C) + (row0 + r) * p.ldc + n, pack_bf16x8(v));
+  }
 }
 
 template <int BM, int BN, int WM, int WN, int BK, int R, int OUT, bool GATHER, bool GROUPED, int GACT,
@@ -1244,8 +1336,15 @@ hipError_t launch_cfg(gemm_params_t<OUT, GROUPED, KM> p, hipStream_t s) {
     if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&o, kernel, WM * WN * 64, 0) != hipSuccess) o = 1;
     return std::max(o, 1);
   }();
-  const int64_t blocks = std::min<int64_t>(tiles, (int64_t)p.cus * per_cu);
+  const int64_t blocks = std::min<int64_t>(tiles * ((KM & kTail) ? kMaxTailParts : 1), (int64_t)p.cus * per_cu);
+  if constexpr ((KM & kTail) != 0) {   // every part has a stage, every block a tile of `tail`
+    if (p.tail == nullptr || p.K < BK * kMaxTailParts || blocks > kMaxTailBlocks) return hipErrorInvalidValue;
+  }
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, s, p);
+  if constexpr ((KM & kTail) != 0) {
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemm_tail_kernel<BM, BN>), dim3((unsigned)blocks), dim3(512), 0, s, p);
+  }
   return hipGetLastError();
 }
 

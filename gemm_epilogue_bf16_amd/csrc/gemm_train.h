@@ -35,6 +35,13 @@ struct GemmProduct {
 // the k rows from there to the split (or to K) are zeros.
 constexpr int kSplitB = 16;
 
+// bit 5: tiles left over after the last whole round of an XCD's blocks, where two or
+// more blocks are there for each, are split over k; the parts go to `tail` in fp32
+// (256 x 256 for each of kMaxTailBlocks blocks at most) and a second launch adds them.
+constexpr int kTail = 32;
+constexpr int kMaxTailParts = 8, kMaxTailBlocks = 256;
+constexpr size_t kTailBytes = (size_t)kMaxTailBlocks * 256 * 256 * 4;
+
 struct GemmTrainParams : GemmParams {
   uint8_t* codes;              // checkpoint: E4M3 codes [rows, 2N], g in columns [0, N), u in [N, 2N)
   uint8_t* qscale;             // and scale exponents (+ 127) [rows, 2 ceil(N / kCkptBlock)]
@@ -42,13 +49,15 @@ struct GemmTrainParams : GemmParams {
   int products;                // kList
   GemmProduct list[kMaxProducts];
   int64_t kb_rows;             // kSplitB
+  float* tail;                 // kTail
   int64_t stride_c;            // ragged: elements between consecutive groups' outputs
   int64_t group_rows;          // grouped, ragged: the rows there are; group_off is the caller's table, unchecked
 };
 
 // Every form below runs on TILE_128x128 or TILE_256x256.
 // y = act(x W[g]^T + b[g]) over each group's rows (GEMM_OUT_BF16), its dz
-// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2).
+// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2, on 256x256
+// tiles also 2 | kTail).
 hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
 hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);

@@ -30,6 +30,10 @@ hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p,
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s)
                : launch_cfg<128, 128, 4, 2, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2>(p, s);
   }
+  if (out_kind == GEMM_OUT_BF16 && p.kmajor == (2 | kTail) && big) {
+    if (p.bias != nullptr || p.act != ACT_NONE) return hipErrorInvalidValue;
+    return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2 | kTail>(p, s);
+  }
   if (p.kmajor != 0) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16)
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s)

@@ -85,11 +85,26 @@ hipError_t run_product(const ProductPlan& plan, GemmTrainParams p, uint16_t* C, 
   return e != hipSuccess ? e : launch_sum_parts(parts, plan.split, p.M * p.N, p.M * p.N, C, s);
 }
 
-// The row tiles of E ragged groups: the sizes are on the device, so the mean
-// R / E stands for them, with half a tile wasted per group.
+// Tiles over E ragged groups' rows: the sizes are on the device, so the mean R / E
+// stands for them, with half a tile wasted per group.
+int64_t grouped_tiles(int64_t R, int64_t N, int32_t E, int t) { return (R / t + (E + 1) / 2) * ((N + t - 1) / t); }
 bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
-  const int64_t t256 = (R / 256 + (E + 1) / 2) * ((N + 255) / 256), t128 = (R / 128 + (E + 1) / 2) * ((N + 127) / 128);
-  return plan_product(t256, t128, (K + 63) / 64, R * N, 1).tile == TILE_256x256;
+  return plan_product(grouped_tiles(R, N, E, 256), grouped_tiles(R, N, E, 128), (K + 63) / 64, R * N, 1).tile == TILE_256x256;
+}
+
+// dx on 256 tiles with the last round's split over a long contraction (kTail): one
+// more launch and the parts' round trip, against up to three quarters of a round.
+// Where the estimated tiles leave two or more blocks for each of that round's.
+// (The three gradients, unsplit in brackets: 8192 rows in 8 groups through
+// 4096 <- 14336, 2.25 rounds, 1848 us (1974); 4096 rows 1136 (1375).)
+constexpr int64_t kTailK = 4096;
+bool grouped_tail(int64_t R, int64_t N, int64_t K, int32_t E) {
+  const int64_t tiles = grouped_tiles(R, N, E, 256), rest = tiles % 256, stages = (K + 63) / 64;
+  const int64_t P = rest > 0 ? std::min<int64_t>(256 / rest, kMaxTailParts) : 1;
+  if (K < kTailK || P < 2) return false;
+  const double t = rounds256(tiles - rest, stages) + kPartsLaunch + rounds256(rest * P, (stages + P - 1) / P) +
+                   8.0 * (double)(P * rest * 256 * 256) / kPartsBytesPerUs;
+  return t < std::min(rounds256(tiles, stages), rounds128(grouped_tiles(R, N, E, 128), stages));
 }
 
 void set_groups(GemmTrainParams& p, const int32_t* group_off, int32_t E, int64_t R, bool big) {
@@ -108,13 +123,16 @@ ProductPlan plan_grouped_dw(int64_t R, int64_t N, int64_t K, int32_t E) {
 struct GroupedBwdLayout {
   size_t dz, parts, total;
   ProductPlan dw;
+  bool dx_big, dx_tail;
 };
 GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, int act) {
   GroupedBwdLayout L;
   L.dw = plan_grouped_dw(R, N, K, E);
+  L.dx_tail = grouped_tail(R, K, N, E);
+  L.dx_big = L.dx_tail || grouped_big(R, K, N, E);
   size_t o = kHeader;   // the decode header stays untouched
   L.dz = o;    o += act != FMLP_ACT_NONE ? ws_bf16(R, N) : 0;
-  L.parts = o; o += parts_bytes(L.dw, E * N * K);
+  L.parts = o; o += std::max(parts_bytes(L.dw, E * N * K), L.dx_tail ? kTailBytes : 0);   // of dx, then of dW
   L.total = o;
   return L;
 }
@@ -198,13 +216,16 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
     dz = dzw;
   }
   {   // dx = dz W[e]: the contraction runs over W's rows, read k-major
-    const bool big = grouped_big(R, K, N, E);
     GemmTrainParams p = train_params(dense_params(dz, N, W, nullptr, nullptr, dx, K, R, K, N, FMLP_ACT_NONE, cus));
-    set_groups(p, group_off, E, R, big);
+    set_groups(p, group_off, E, R, L.dx_big);
     p.strideB = N * K;
     p.kmajor = 2;
+    if (L.dx_tail && cus <= kMaxTailBlocks) {
+      p.kmajor |= kTail;
+      p.tail = reinterpret_cast<float*>(ws + L.parts);
+    }
     p.ldb = K;
-    HIP_TRY(launch_gemm_grouped(GEMM_OUT_BF16, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dx launch");
+    HIP_TRY(launch_gemm_grouped(GEMM_OUT_BF16, L.dx_big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dx launch");
   }
   {   // dW[e] = dz^T x over the group's rows, both read k-major
     float* parts = reinterpret_cast<float*>(ws + L.parts);

@@ -68,6 +68,25 @@ def test_forward_and_gradients(shape, act, bias):
     assert again[2] is None if not bias else torch.equal(again[2], db)
 
 
+# dx's last tiles in 2 and 4 parts of a long contraction, whole rounds before them and none; rows of nobody
+@pytest.mark.parametrize("rows,K,N", [([1000, 1100, 950, 1146, 900, 1096, 1000, 1000], 2056, 4104), ([0, 8000, 0, 31], 2056, 4104),
+                                      ([1024, 1024, 1024, 1024], 1032, 4104), ([13, 4200, 1], 1032, 4168)])
+def test_split_last_round(rows, K, N):
+    import gemm_epilogue_bf16_amd as F
+
+    t, off, offs = make(rows, 3, 2, K, N, False, seed=6)
+    d = dbl(t)
+    dx = torch.full(t["x"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    dW = torch.empty_like(t["W"])
+    F.fmlp_grouped_linear_bwd(t["x"], offs, t["W"], None, "none", t["dy"], out=(dx, dW, None))
+    want, bound = ffn64.grouped_bwd(d["x"], off, d["W"], None, "none", d["dy"])
+    ffn64.check("dx", dx, want[0], bound[0])
+    ffn64.check("dW", dW, want[1], bound[1])
+    assert bool((dx[:3] == 7.0).all()) and bool((dx[-2:] == 7.0).all())
+    again = F.fmlp_grouped_linear_bwd(t["x"], offs, t["W"], None, "none", t["dy"])
+    assert torch.equal(again[0][3:-2], dx[3:-2])
+
+
 def test_gradient_agrees_with_differences():
     """The GPU's gradients against central differences of the 64-bit forward along random directions.  The difference
     quotient is off by h^2/6 of the third derivative and by rounding / h; what remains is the gradient's own bound."""
