@@ -47,7 +47,7 @@
 // LDS in wave order (deterministic).
 //
 // Activations live in LDS as records, one per chunk: hi and lo of every token in
-// operand order, their exponents, and the groups' sums.  Up to 64 of them
+// operand order, their exponents, and the groups' sums.  Up to 160 of them
 // (tokens x chunks) a block makes its own from x, while its first weights are
 // in flight; more are made once per call by a small kernel into the workspace
 // and copied to LDS.  Where all records do not fit, k is cut into slices that
@@ -74,6 +74,11 @@ namespace {
 constexpr int kWaves = 16;   // one block a CU
 constexpr int kThreads = kWaves * 64;
 constexpr int kChunk = 128;   // k of one 16-byte load of the 4 lanes of a row
+// Tokens x chunks whose records a block makes itself, up to three passes of its
+// threads, all of x's values requested before the weights.  Against the small kernel's
+// launch: 96 units 5.6 us (6.8), 128 11.4 (12.4), 160 12.3 (13.2), but 192 8.1
+// (7.7) and 8.8 (8.2).
+constexpr int kUnitsInside = 160;
 
 // A raw buffer of `bytes` at base, both wave-uniform: readfirstlane says so to
 // the compiler, which computes tile addresses on the vector unit and would
@@ -477,20 +482,21 @@ __global__ __launch_bounds__(kThreads) void decode_w4_kernel(W4Layer L, int M, W
   } else {
     // 16 lanes a unit (chunk u / M, token u % M)
     constexpr int kUnits = kThreads / 16;
+    static_assert(kUnitsInside <= 3 * kUnits, "three passes");
     const int i16 = threadIdx.x & 15;
     auto fetch = [&](int u) {
       const int c = u / M, k = (cb + c) * kChunk + i16 * 8;
       return u < M * chunks && k < K ? ld16(L.x + (int64_t)(u - c * M) * K + k) : zero4();
     };
     int u = threadIdx.x >> 4;
-    u32x4_t xv = fetch(u), xn = fetch(u + kUnits);
+    u32x4_t xv = fetch(u), xn = fetch(u + kUnits), xo = fetch(u + 2 * kUnits);
     issue(A);
 #pragma clang loop unroll(disable)
     for (; u < M * chunks; u += kUnits) {
       const int c = u / M;
       put_record<GS, ZEROS>(lds + c * R.bytes, R, xv, u - c * M, M, i16);
       xv = xn;
-      xn = fetch(u + 2 * kUnits);
+      xn = xo;
     }
   }
   lds_barrier();
@@ -521,7 +527,6 @@ __global__ __launch_bounds__(256) void w4_sum_kernel(W4Layer L, int M, W4Cut cut
 }
 
 constexpr int64_t kLdsMax = 160 * 1024;   // of a block, one a CU
-constexpr int kUnitsInside = 64;          // tokens x chunks whose records a block makes itself: one pass of its threads
 
 int log2_group(int G) { return G == 32 ? 5 : G == 64 ? 6 : 7; }
 int64_t red_bytes(int64_t M, bool dual) { return (int64_t)kWaves * (dual ? 2 : 1) * (M <= 8 ? 32 : 64) * 16; }
