@@ -354,16 +354,17 @@ __device__ __forceinline__ int blocks_before_xcd(int G, int x) {
   const int q = G / kNumXcd, r = G % kNumXcd;
   return x * q + min(x, r);
 }
-// kTail: how an XCD's n tiles run on its nb blocks: whole rounds, then `rest` tiles
-// in `parts` parts of the k range each, one per block (1: the rest runs unsplit).
+// kTail: how an XCD's n tiles of `stages` 64-k stages run on its nb blocks: whole
+// rounds, then `rest` tiles in `parts` parts of the k range each, of kTailStages or
+// more, one per block (1: the rest runs unsplit).
 struct TailCut {
   int full, rest, parts;
 };
-__device__ __forceinline__ TailCut tail_cut(int n, int nb) {
+__device__ __forceinline__ TailCut tail_cut(int n, int nb, int stages) {
   TailCut c;
   c.full = n / nb * nb;
   c.rest = n - c.full;
-  c.parts = c.rest > 0 ? min(nb / c.rest, kMaxTailParts) : 1;
+  c.parts = c.rest > 0 ? max(min(nb / c.rest, min(stages / kTailStages, kMaxTailParts)), 1) : 1;
   return c;
 }
 
@@ -491,7 +492,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
   int nmine = xj < t_hi - t_lo ? (t_hi - t_lo - xj + nbx - 1) / nbx : 0;
   TailCut cut{0, 0, 1};
   if constexpr (TAIL) {
-    cut = tail_cut(t_hi - t_lo, nbx);
+    cut = tail_cut(t_hi - t_lo, nbx, (Kc + BK - 1) / BK);
     nmine = cut.full / nbx + (xj < cut.rest * cut.parts ? 1 : 0);
   }
   if (nmine == 0) return;   // block-uniform: no barrier has been reached
@@ -1262,7 +1263,7 @@ __global__ void __launch_bounds__(512) gemm_tail_kernel(GemmTrainParams p) {
   const int64_t total = (int64_t)tiles_m * p.tiles_n;
   const int b0 = blocks_before_xcd(G, xcd), b1 = blocks_before_xcd(G, xcd + 1);
   const int t_lo = (int)(total * b0 / G), t_hi = (int)(total * b1 / G);
-  const TailCut cut = tail_cut(t_hi - t_lo, b1 - b0);
+  const TailCut cut = tail_cut(t_hi - t_lo, b1 - b0, (int)((p.K + 63) / 64));
   if (cut.parts == 1 || xj >= cut.rest * cut.parts) return;
   int tm, tn;
   grouped_tile(t_lo + cut.full + xj / cut.parts, tiles_m, p.tiles_n, p.group_m, tm, tn);
@@ -1337,8 +1338,9 @@ hipError_t launch_cfg(gemm_params_t<OUT, GROUPED, KM> p, hipStream_t s) {
     return std::max(o, 1);
   }();
   const int64_t blocks = std::min<int64_t>(tiles * ((KM & kTail) ? kMaxTailParts : 1), (int64_t)p.cus * per_cu);
-  if constexpr ((KM & kTail) != 0) {   // every part has a stage, every block a tile of `tail`
-    if (p.tail == nullptr || p.K < BK * kMaxTailParts || blocks > kMaxTailBlocks) return hipErrorInvalidValue;
+  if constexpr ((KM & kTail) != 0) {   // every block has a tile of `tail`
+    static_assert(BK == 64, "64-k stages");
+    if (p.tail == nullptr || blocks > kMaxTailBlocks) return hipErrorInvalidValue;
   }
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, s, p);
   if constexpr ((KM & kTail) != 0) {

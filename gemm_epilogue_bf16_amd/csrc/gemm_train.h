@@ -39,7 +39,7 @@ constexpr int kSplitB = 16;
 // more blocks are there for each, are split over k; the parts go to `tail` in fp32
 // (256 x 256 for each of kMaxTailBlocks blocks at most) and a second launch adds them.
 constexpr int kTail = 32;
-constexpr int kMaxTailParts = 8, kMaxTailBlocks = 256;
+constexpr int kMaxTailParts = 32, kTailStages = 4, kMaxTailBlocks = 256;
 constexpr size_t kTailBytes = (size_t)kMaxTailBlocks * 256 * 256 * 4;
 
 struct GemmTrainParams : GemmParams {

@@ -97,10 +97,10 @@ bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
 // Where the estimated tiles leave two or more blocks for each of that round's.
 // (The three gradients, unsplit in brackets: 8192 rows in 8 groups through
 // 4096 <- 14336, 2.25 rounds, 1848 us (1974); 4096 rows 1136 (1375).)
-constexpr int64_t kTailK = 4096;
+constexpr int64_t kTailK = 1024;
 bool grouped_tail(int64_t R, int64_t N, int64_t K, int32_t E) {
   const int64_t tiles = grouped_tiles(R, N, E, 256), rest = tiles % 256, stages = (K + 63) / 64;
-  const int64_t P = rest > 0 ? std::min<int64_t>(256 / rest, kMaxTailParts) : 1;
+  const int64_t P = rest > 0 ? std::min<int64_t>({256 / rest, stages / kTailStages, kMaxTailParts}) : 1;
   if (K < kTailK || P < 2) return false;
   const double t = rounds256(tiles - rest, stages) + kPartsLaunch + rounds256(rest * P, (stages + P - 1) / P) +
                    8.0 * (double)(P * rest * 256 * 256) / kPartsBytesPerUs;
