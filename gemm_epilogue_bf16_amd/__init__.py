@@ -167,11 +167,12 @@ def lib() -> ctypes.CDLL:
         L.fmlp_glu_ckpt.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]
         L.fmlp_glu_ckpt_bwd.argtypes = [_p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p,
                                         _sz, _p]
-        L.fmlp_grouped_linear.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _p, _p]
+        L.fmlp_grouped_linear.argtypes = [_p, _p, _p, _p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _p, _p, _sz, _p]
         L.fmlp_grouped_linear_bwd.argtypes = [_p, _p, _p, _p, ctypes.c_int, _p, _i64, _i64, _i64, ctypes.c_int32, _p, _p,
                                               _p, _p, _sz, _p]
         for f, a in (("fmlp_glu_ckpt_workspace_size", [_i64] * 3), ("fmlp_glu_ckpt_bwd_workspace_size", [_i64] * 3),
                      ("fmlp_glu_ckpt_codes_size", [_i64] * 2), ("fmlp_glu_ckpt_scales_size", [_i64] * 2),
+                     ("fmlp_grouped_linear_workspace_size", [_i64] * 3 + [ctypes.c_int32]),
                      ("fmlp_grouped_linear_bwd_workspace_size", [_i64] * 3 + [ctypes.c_int32, ctypes.c_int])):
             getattr(L, f).argtypes = a
             getattr(L, f).restype = _sz
@@ -601,23 +602,29 @@ def _grouped_args(device, x, group_off, W, b):
     return R, K, N, E
 
 
-def _grouped_linear_call(device, x, group_off, W, b, act, out):
+@functools.lru_cache(maxsize=1024)
+def _grouped_linear_need(R, K, N, E) -> int:
+    return lib().fmlp_grouped_linear_workspace_size(R, K, N, E)
+
+
+def _grouped_linear_call(device, x, group_off, W, b, act, out, workspace):
     R, K, N, E = _grouped_args(device, x, group_off, W, b)
     y = _out("out", out, (R, N), device)
+    ws, wp, wn = _scratch(device, workspace, _grouped_linear_need(R, K, N, E))
     return (lib().fmlp_grouped_linear, (x.data_ptr(), group_off.data_ptr(), W.data_ptr(), _ptr(b), ACT[act], R, K, N, E,
-                                        y.data_ptr(), _raw_stream(device)), y, (x, group_off, W, b))
+                                        y.data_ptr(), wp, wn, _raw_stream(device)), y, (x, group_off, W, b, ws))
 
 
-def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None):
+def fmlp_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None):
     """y[r] = act(x[r] W[e]^T + b[e]) for the rows [group_off[e], group_off[e+1]) of every group e.
 
     x [R, K]; group_off int32 [E + 1] on the device; W [E, N, K]; b [E, N] or None -> y [R, N].  Rows outside every
     group are not written: with out=None they hold whatever the new tensor held."""
-    return _call(x, _grouped_linear_call, group_off, W, b, act, out)
+    return _call(x, _grouped_linear_call, group_off, W, b, act, out, workspace)
 
 
-def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None) -> BoundCall:
-    return _bind(x, _grouped_linear_call, group_off, W, b, act, out)
+def bind_grouped_linear(x, group_off, W, b=None, act: str = "none", out=None, workspace=None) -> BoundCall:
+    return _bind(x, _grouped_linear_call, group_off, W, b, act, out, workspace)
 
 
 def _grouped_linear_bwd_call(device, x, group_off, W, b, act, dy, out, workspace):

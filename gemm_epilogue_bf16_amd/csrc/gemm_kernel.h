@@ -418,7 +418,7 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
                 "k-major operands: tiles of 128 or 256 columns, wave tiles 64 wide, 16x16x32 MFMAs, one weight set");
   constexpr bool TAIL = (KM & kTail) != 0;
   static_assert(!GROUPED || (KM & ~kTail) == 0 || (KM & ~kTail) == 2, "grouped rows: only the weights k-major");
-  static_assert(!TAIL || (GROUPED && OUT == GEMM_OUT_BF16), "split last round: grouped rows, bf16");
+  static_assert(!TAIL || (GROUPED && (OUT == GEMM_OUT_BF16 || OUT == GEMM_OUT_DACT)), "split last round: grouped rows");
   static_assert(!RAGK || (KMA && KMB && !GROUPED), "ragged k ranges: both operands k-major");
   static_assert(!(OUT == GEMM_OUT_GLU_SAVE && M32) && kCkptBlock == 32, "a checkpoint block is one run of 4 lane groups");
 
@@ -1252,8 +1252,8 @@ gemm_bf16_kernel(gemm_params_t<OUT, GROUPED, KM> p) {
 
 // kTail's second launch, with the first one's grid: the block that made part kp of a
 // split tile adds a share of the tile's rows over its parts, in their order, and
-// rounds once.
-template <int BM, int BN>
+// applies the epilogue's bias and activation (or its derivative) and rounds once.
+template <int BM, int BN, int OUT, int GACT>
 __global__ void __launch_bounds__(512) gemm_tail_kernel(GemmTrainParams p) {
   __shared__ GroupTables<false> tables;
   make_group_tables(tables, p.group_off, p.groups, (int32_t)p.group_rows, BM, 1);
@@ -1279,6 +1279,8 @@ __global__ void __launch_bounds__(512) gemm_tail_kernel(GemmTrainParams p) {
   const int64_t n = (int64_t)tn * BN + c;
   if (n >= p.N) return;   // N % 8 == 0
   const int end = min(rows, (kp + 1) * BM / cut.parts);
+  float bias[8] = {};
+  if (p.bias) unpack_bf16x8(ld16(p.bias + lo * p.stride_bias + n), bias);
   for (int r = kp * BM / cut.parts + threadIdx.x / (BN / 8); r < end; r += 512 / (BN / 8)) {
     float v[8] = {};
     for (int j = 0; j < cut.parts; ++j) {
@@ -1289,6 +1291,21 @@ __global__ void __launch_bounds__(512) gemm_tail_kernel(GemmTrainParams p) {
         v[e] += __uint_as_float(a[e]);
         v[4 + e] += __uint_as_float(b[e]);
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    if constexpr (OUT == GEMM_OUT_DACT) {
+      float dy[8];
+      unpack_bf16x8(ld16(p.E + (row0 + r) * p.lde + n), dy);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float a, da;
+        act_and_grad<GACT>(v[e], a, da);
+        v[e] = dy[e] * da;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = apply_act(v[e], p.act);
     }
     st16(static_cast<uint16_t*>(p.C) + (row0 + r) * p.ldc + n, pack_bf16x8(v));
   }
@@ -1345,7 +1362,7 @@ hipError_t launch_cfg(gemm_params_t<OUT, GROUPED, KM> p, hipStream_t s) {
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, s, p);
   if constexpr ((KM & kTail) != 0) {
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((gemm_tail_kernel<BM, BN>), dim3((unsigned)blocks), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((gemm_tail_kernel<BM, BN, OUT, GACT>), dim3((unsigned)blocks), dim3(512), 0, s, p);
   }
   return hipGetLastError();
 }

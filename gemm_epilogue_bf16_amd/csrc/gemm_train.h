@@ -56,8 +56,8 @@ struct GemmTrainParams : GemmParams {
 
 // Every form below runs on TILE_128x128 or TILE_256x256.
 // y = act(x W[g]^T + b[g]) over each group's rows (GEMM_OUT_BF16), its dz
-// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2, on 256x256
-// tiles also 2 | kTail).
+// (GEMM_OUT_DACT), or dx = dz W[g] (GEMM_OUT_BF16 with kmajor = 2); on 256x256
+// tiles also with kmajor | kTail.
 hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);
 // The ragged weight gradient (kmajor = 3 | kKmajorRagged), bf16 or split fp32.
 hipError_t launch_gemm_ragged(int out_kind, int tile, const GemmTrainParams& p, hipStream_t s);

@@ -34,6 +34,13 @@ hipError_t launch_gemm_grouped(int out_kind, int tile, const GemmTrainParams& p,
     if (p.bias != nullptr || p.act != ACT_NONE) return hipErrorInvalidValue;
     return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, 2 | kTail>(p, s);
   }
+  if (p.kmajor == kTail && big) {
+    if (out_kind == GEMM_OUT_BF16) return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE, false, kTail>(p, s);
+    if (out_kind == GEMM_OUT_DACT)
+      return by_act(p.act, [&](auto a) {
+        return launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_DACT, false, true, a.value, false, kTail>(p, s);
+      });
+  }
   if (p.kmajor != 0) return hipErrorInvalidValue;
   if (out_kind == GEMM_OUT_BF16)
     return big ? launch_cfg<256, 256, 2, 4, 64, 2, GEMM_OUT_BF16, false, true, ACT_NONE>(p, s)

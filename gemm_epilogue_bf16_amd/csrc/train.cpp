@@ -92,7 +92,7 @@ bool grouped_big(int64_t R, int64_t N, int64_t K, int32_t E) {
   return plan_product(grouped_tiles(R, N, E, 256), grouped_tiles(R, N, E, 128), (K + 63) / 64, R * N, 1).tile == TILE_256x256;
 }
 
-// dx on 256 tiles with the last round's split over a long contraction (kTail): one
+// 256 tiles with the last round's split over a long contraction (kTail): one
 // more launch and the parts' round trip, against up to three quarters of a round.
 // Where the estimated tiles leave two or more blocks for each of that round's.
 // (The three gradients, unsplit in brackets: 8192 rows in 8 groups through
@@ -105,6 +105,22 @@ bool grouped_tail(int64_t R, int64_t N, int64_t K, int32_t E) {
   const double t = rounds256(tiles - rest, stages) + kPartsLaunch + rounds256(rest * P, (stages + P - 1) / P) +
                    8.0 * (double)(P * rest * 256 * 256) / kPartsBytesPerUs;
   return t < std::min(rounds256(tiles, stages), rounds128(grouped_tiles(R, N, E, 128), stages));
+}
+
+// Tile of a grouped product over K, and whether its last round is split.
+struct GroupedPlan {
+  bool big, tail;
+};
+GroupedPlan plan_grouped(int64_t R, int64_t N, int64_t K, int32_t E) {
+  const bool tail = grouped_tail(R, N, K, E);
+  return {tail || grouped_big(R, N, K, E), tail};
+}
+hipError_t run_grouped(int out_kind, const GroupedPlan& plan, GemmTrainParams p, float* tail, hipStream_t s) {
+  if (plan.tail && p.cus <= kMaxTailBlocks) {
+    p.kmajor |= kTail;
+    p.tail = tail;
+  }
+  return launch_gemm_grouped(out_kind, plan.big ? TILE_256x256 : TILE_128x128, p, s);
 }
 
 void set_groups(GemmTrainParams& p, const int32_t* group_off, int32_t E, int64_t R, bool big) {
@@ -123,16 +139,16 @@ ProductPlan plan_grouped_dw(int64_t R, int64_t N, int64_t K, int32_t E) {
 struct GroupedBwdLayout {
   size_t dz, parts, total;
   ProductPlan dw;
-  bool dx_big, dx_tail;
+  GroupedPlan dzp, dxp;
 };
 GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, int act) {
   GroupedBwdLayout L;
   L.dw = plan_grouped_dw(R, N, K, E);
-  L.dx_tail = grouped_tail(R, K, N, E);
-  L.dx_big = L.dx_tail || grouped_big(R, K, N, E);
+  L.dzp = plan_grouped(R, N, K, E);
+  L.dxp = plan_grouped(R, K, N, E);
   size_t o = kHeader;   // the decode header stays untouched
   L.dz = o;    o += act != FMLP_ACT_NONE ? ws_bf16(R, N) : 0;
-  L.parts = o; o += std::max(parts_bytes(L.dw, E * N * K), L.dx_tail ? kTailBytes : 0);   // of dx, then of dW
+  L.parts = o; o += std::max(parts_bytes(L.dw, E * N * K), L.dxp.tail || (act != FMLP_ACT_NONE && L.dzp.tail) ? kTailBytes : 0);   // of one product at a time
   L.total = o;
   return L;
 }
@@ -141,8 +157,14 @@ GroupedBwdLayout grouped_bwd_layout(int64_t R, int64_t K, int64_t N, int32_t E, 
 
 extern "C" {
 
+size_t fmlp_grouped_linear_workspace_size(int64_t R, int64_t K, int64_t N, int32_t E) {
+  if (R <= 0 || K <= 0 || N <= 0 || E < 1 || E > kMaxGroups) return 0;
+  return plan_grouped(R, N, K, E).tail ? kHeader + kTailBytes : 0;
+}
+
 fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W, const fmlp_bf16* b,
-                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, fmlp_stream stream) {
+                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, void* workspace,
+                                size_t workspace_bytes, fmlp_stream stream) {
   TRY(check_rows("R", R));
   TRY(check_inner("K", K));
   TRY(check_inner("N", N));
@@ -153,16 +175,18 @@ fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, co
   REQUIRE_PTR(W);
   OPTIONAL_PTR(b);
   TOKEN_PTR(y, R);
+  if (const size_t need = fmlp_grouped_linear_workspace_size(R, K, N, E)) TRY(check_workspace(workspace, workspace_bytes, need));
   if (R == 0) return ok();
   int cus = 0;
   TRY(check_device(&cus));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool big = grouped_big(R, N, K, E);
+  const GroupedPlan plan = plan_grouped(R, N, K, E);
   GemmTrainParams p = train_params(dense_params(x, K, W, nullptr, b, y, N, R, N, K, act, cus));
-  set_groups(p, group_off, E, R, big);
+  set_groups(p, group_off, E, R, plan.big);
   p.strideB = N * K;
   p.stride_bias = N;
-  return launched(launch_gemm_grouped(GEMM_OUT_BF16, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear launch");
+  float* tail = plan.tail ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader) : nullptr;
+  return launched(run_grouped(GEMM_OUT_BF16, plan, p, tail, s), "grouped_linear launch");
 }
 
 size_t fmlp_grouped_linear_bwd_workspace_size(int64_t R, int64_t K, int64_t N, int32_t E, int act) {
@@ -202,33 +226,28 @@ fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off
     return ok();
   }
   char* ws = static_cast<char*>(workspace);
+  float* parts = reinterpret_cast<float*>(ws + L.parts);
   const uint16_t* dz = dy;
   if (act != FMLP_ACT_NONE) {   // dz = dy * act'(x W^T + b), z recomputed
     uint16_t* dzw = reinterpret_cast<uint16_t*>(ws + L.dz);
-    const bool big = grouped_big(R, N, K, E);
     GemmTrainParams p = train_params(dense_params(x, K, W, nullptr, b, dzw, N, R, N, K, act, cus));
-    set_groups(p, group_off, E, R, big);
+    set_groups(p, group_off, E, R, L.dzp.big);
     p.strideB = N * K;
     p.stride_bias = N;
     p.E = dy;
     p.lde = N;
-    HIP_TRY(launch_gemm_grouped(GEMM_OUT_DACT, big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dz launch");
+    HIP_TRY(run_grouped(GEMM_OUT_DACT, L.dzp, p, parts, s), "grouped_linear_bwd dz launch");
     dz = dzw;
   }
   {   // dx = dz W[e]: the contraction runs over W's rows, read k-major
     GemmTrainParams p = train_params(dense_params(dz, N, W, nullptr, nullptr, dx, K, R, K, N, FMLP_ACT_NONE, cus));
-    set_groups(p, group_off, E, R, L.dx_big);
+    set_groups(p, group_off, E, R, L.dxp.big);
     p.strideB = N * K;
     p.kmajor = 2;
-    if (L.dx_tail && cus <= kMaxTailBlocks) {
-      p.kmajor |= kTail;
-      p.tail = reinterpret_cast<float*>(ws + L.parts);
-    }
     p.ldb = K;
-    HIP_TRY(launch_gemm_grouped(GEMM_OUT_BF16, L.dx_big ? TILE_256x256 : TILE_128x128, p, s), "grouped_linear_bwd dx launch");
+    HIP_TRY(run_grouped(GEMM_OUT_BF16, L.dxp, p, parts, s), "grouped_linear_bwd dx launch");
   }
   {   // dW[e] = dz^T x over the group's rows, both read k-major
-    float* parts = reinterpret_cast<float*>(ws + L.parts);
     const bool split = L.dw.split > 1;
     GemmTrainParams p = train_params(dense_params(dz, N, x, nullptr, nullptr, split ? static_cast<void*>(parts) : dW, K, N,
                                                   K, R, FMLP_ACT_NONE, cus));

@@ -290,11 +290,15 @@ size_t fmlp_glu_ckpt_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
  * group are left as they were.  R K, R N and N K must each be below 2^30
  * (FMLP_E_SHAPE).  Both operands of dW and the weights of dx are read as
  * stored.  Bitwise deterministic.
- * The forward is one launch without a workspace; the backward's needs no
- * initialisation, and its first 8192 bytes are left alone.
+ * The forward is one launch, or two where few tiles over a long contraction are
+ * split (its parts are added in fp32 in a fixed order).  The workspaces
+ * (fmlp_grouped_linear: NULL where its size is 0) need no initialisation, and
+ * their first 8192 bytes are left alone.
  */
 fmlp_status fmlp_grouped_linear(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W, const fmlp_bf16* b,
-                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, fmlp_stream stream);
+                                int act, int64_t R, int64_t K, int64_t N, int32_t E, fmlp_bf16* y, void* workspace,
+                                size_t workspace_bytes, fmlp_stream stream);
+size_t fmlp_grouped_linear_workspace_size(int64_t R, int64_t K, int64_t N, int32_t E);
 fmlp_status fmlp_grouped_linear_bwd(const fmlp_bf16* x, const int32_t* group_off, const fmlp_bf16* W,
                                     const fmlp_bf16* b, int act, const fmlp_bf16* dy, int64_t R, int64_t K, int64_t N,
                                     int32_t E, fmlp_bf16* dx, fmlp_bf16* dW, fmlp_bf16* db, void* workspace,

@@ -24,8 +24,8 @@ def _err(L):
     return L.fmlp_last_error().decode()
 
 
-def grouped(L, x=X, off=O, w=W, b=B, act=1, R=40, K=64, N=72, E=4, y=Y):
-    return L.fmlp_grouped_linear(x, off, w, b, act, R, K, N, E, y, None)
+def grouped(L, x=X, off=O, w=W, b=B, act=1, R=40, K=64, N=72, E=4, y=Y, ws=WS, nb=BIG):
+    return L.fmlp_grouped_linear(x, off, w, b, act, R, K, N, E, y, ws, nb, None)
 
 
 def grouped_bwd(L, x=X, off=O, w=W, b=B, act=1, dy=Y, R=40, K=64, N=72, E=4, dx=Y, dW=Y, db=B, ws=WS, nb=BIG):
@@ -42,7 +42,13 @@ COMMON = [
 ]
 
 
-@pytest.mark.parametrize("kw,status,msg", COMMON + [(dict(y=None), E_NULL, "y is NULL")])
+LONG = dict(R=200, K=8192, N=1024, E=1)   # few tiles over a long contraction: split, with a workspace
+
+
+@pytest.mark.parametrize("kw,status,msg", COMMON + [
+    (dict(y=None), E_NULL, "y is NULL"), (dict(LONG, ws=None, nb=0), E_WS, "NULL"), (dict(LONG, nb=16), E_WS, "needs"),
+    (dict(LONG, ws=WS + 8), E_ALIGN, "workspace"),
+])
 def test_grouped_validation(L, kw, status, msg):
     assert grouped(L, **kw) == status and msg in _err(L)
 
@@ -60,10 +66,14 @@ def test_grouped_bwd_validation(L, kw, status, msg):
 
 def test_grouped_no_rows_is_a_noop(L):
     assert grouped(L, x=None, R=0, y=None) == OK
+    assert grouped(L, x=None, R=0, y=None, ws=None, nb=0) == OK
     assert grouped(L, x=None, R=0, y=None, w=None) == E_NULL
 
 
 def test_grouped_sizes(L):
+    assert L.fmlp_grouped_linear_workspace_size(40, 64, 72, 4) == 0
+    assert L.fmlp_grouped_linear_workspace_size(0, 8192, 1024, 1) == 0
+    assert L.fmlp_grouped_linear_workspace_size(*(LONG[k] for k in "RKNE")) == 8192 + 256 * 256 * 256 * 4
     assert L.fmlp_grouped_linear_bwd_workspace_size(40, 64, 72, 4, 0) == 8192
     assert L.fmlp_grouped_linear_bwd_workspace_size(40, 64, 72, 4, 1) == 8192 + 40 * 72 * 2 + 128   # dz
     # 4 groups of one tile each over about 8192 rows: split, a multiple of the gradient's fp32 size

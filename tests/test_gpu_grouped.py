@@ -68,6 +68,54 @@ def test_forward_and_gradients(shape, act, bias):
     assert again[2] is None if not bias else torch.equal(again[2], db)
 
 
+# few tiles over a long contraction, in up to 32 parts, a ragged last part, a group of one row and an empty one
+@pytest.mark.parametrize("rows,K,N", [([200], 8200, 1032), ([1, 0, 90, 300], 4104, 264), ([257], 6152, 520), ([3], 9000, 8)])
+@pytest.mark.parametrize("act", ffn64.ACTS)
+def test_split_contraction(rows, K, N, act):
+    import gemm_epilogue_bf16_amd as F
+
+    t, off, offs = make(rows, 1, 2, K, N, act != "relu", seed=7)
+    d = dbl(t)
+    y = torch.full(t["dy"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    F.fmlp_grouped_linear(t["x"], offs, t["W"], t["b"], act, out=y)
+    want, bound = ffn64.grouped(d["x"], off, d["W"], d["b"], act)
+    ffn64.check("y", y, want, bound)
+    assert bool((y[:1] == 7.0).all()) and bool((y[-2:] == 7.0).all())
+    assert torch.equal(F.fmlp_grouped_linear(t["x"], offs, t["W"], t["b"], act)[1:-2], y[1:-2])
+    got = F.fmlp_grouped_linear_bwd(t["x"], offs, t["W"], t["b"], act, t["dy"])
+    want, bound = ffn64.grouped_bwd(d["x"], off, d["W"], d["b"], act, d["dy"])
+    for n, a, w, e in zip(("dx", "dW", "db"), got, want, bound):
+        if a is not None:
+            ffn64.check(n, a, w, e)
+
+
+def test_split_contraction_without_rows_and_under_capture():
+    """The tables are the device's: a replayed graph follows them, down to groups without rows."""
+    import gemm_epilogue_bf16_amd as F
+
+    t, off, offs = make([120, 80], 0, 0, 4104, 264, True, seed=8)
+    call = lambda: F.fmlp_grouped_linear(t["x"], offs, t["W"], t["b"], "silu", out=y)   # noqa: E731
+    y = torch.zeros_like(t["dy"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for cut in ((0, 120, 200), (0, 0, 200), (5, 5, 5), (0, 200, 200)):
+        offs.copy_(torch.tensor(cut, dtype=torch.int32))
+        y.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        y.fill_(3.0)
+        call()
+        assert torch.equal(got, y), cut
+        assert cut != (5, 5, 5) or bool((y == 3.0).all())
+
+
 # dx's last tiles in 2 and 4 parts of a long contraction, whole rounds before them and none; rows of nobody
 @pytest.mark.parametrize("rows,K,N", [([1000, 1100, 950, 1146, 900, 1096, 1000, 1000], 2056, 4104), ([0, 8000, 0, 31], 2056, 4104),
                                       ([1024, 1024, 1024, 1024], 1032, 4104), ([13, 4200, 1], 1032, 4168)])
