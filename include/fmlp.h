@@ -280,7 +280,8 @@ size_t fmlp_glu_ckpt_bwd_workspace_size(int64_t M, int64_t D, int64_t H);
  * were.  A table that breaks these rules gives unspecified rows (offsets are
  * clamped into [0, R] and to a running maximum): nothing outside the buffers is
  * touched.  1 <= E <= 1024.  Accumulation in fp32, one rounding to bf16;
- * deterministic: a row's result depends on its own group only.
+ * deterministic.  A row's result depends on its own group only, but for its last
+ * bit: how a sum over K is cut into parts follows the whole table.
  *
  * fmlp_grouped_linear_bwd gives the gradients for an upstream dy [R, N]:
  *   dz = dy * act'(x W[e]^T + b[e]) (recomputed, rounded to bf16 once),
